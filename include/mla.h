@@ -300,6 +300,166 @@ MLA_API int mla_cache_append_paged(const mla_dims* dims, int32_t hidden, const v
                                    int32_t* seqlens, void* workspace, size_t workspace_bytes,
                                    void* stream);
 
+/* --- rotary positions ------------------------------------------------------------
+ * [MLA-とは] "Decoupled RoPE" fixes the rotation R_j and the query/key parts it
+ * applies to; the pair layouts and the scalings for contexts longer than the
+ * trained one have no counterpart on the pages.  mla_rope_init fills a
+ * caller-owned HOST table from the parameters (no device work); the table is
+ * passed by value to the kernels, so it may be changed or freed after a call.
+ *   pair k (k < d_r/2) of a row x: (x[k], x[k + d_r/2]) in MLA_ROPE_HALF,
+ *   (x[2k], x[2k+1]) in MLA_ROPE_INTERLEAVED; rotated in place of the pair.
+ *   f_k = base^(-2k/d_r) radians per position, then by `scaling`:
+ *     MLA_ROPE_LINEAR  f_k / factor
+ *     MLA_ROPE_NTK     base' = base * factor^(d_r / (d_r - 2)) in f_k's place of base (d_r > 2)
+ *     MLA_ROPE_YARN    f_k (1 - g_k) + g_k f_k / factor, with the ramp g_k =
+ *                      clamp((k - low) / max(high - low, 1e-3), 0, 1) between
+ *                      low = max(floor(at(beta_fast)), 0) and
+ *                      high = min(ceil(at(beta_slow)), d_r - 1),
+ *                      at(n) = d_r ln(original_len / (2 pi n)) / (2 ln base)
+ *   amplitude a = attention_factor if that is > 0, else 0.1 ln(factor) + 1 for
+ *   MLA_ROPE_YARN and 1 otherwise; it multiplies the rotated values.
+ * mla_rope: y = a R(pos) x for every row of n_tokens x H rows of d_r values
+ * (transpose = 0), or a R(pos)^T x (transpose = 1: the gradient of y by x
+ * applied to x).  Row (t, h) starts at x + t * x_token_stride + h *
+ * x_head_stride (elements; rows of one head may lie inside wider ones, e.g.
+ * the last d_r of d_nope + d_r); y likewise.  pos [n_tokens] int32, any value
+ * (angles are exact fractions of a turn at any position).  In place (y = x,
+ * same strides) is allowed, other overlaps are not.  dtype MLA_BF16 or
+ * MLA_F32; x and y need only their element's alignment (16-byte aligned rows
+ * with d_r % 16 == 0 are faster); rows of y must not overlap.
+ * mla_rope_init: MLA_ERR_INVALID_ARG for an odd d_r or one outside [2, 256], an
+ * unknown layout or scaling, base <= 1, factor < 1, or for YaRN original_len
+ * <= 0 or betas that are not beta_fast > beta_slow > 0. */
+enum { MLA_ROPE_HALF = 0, MLA_ROPE_INTERLEAVED = 1 };
+enum { MLA_ROPE_UNSCALED = 0, MLA_ROPE_LINEAR = 1, MLA_ROPE_NTK = 2, MLA_ROPE_YARN = 3 };
+typedef struct {
+  int32_t d_r;
+  int32_t layout;           /* MLA_ROPE_HALF or MLA_ROPE_INTERLEAVED */
+  int32_t scaling;          /* MLA_ROPE_UNSCALED ... MLA_ROPE_YARN */
+  float base;
+  float factor;             /* unused when unscaled */
+  float original_len;       /* YaRN: the context length trained on */
+  float beta_fast, beta_slow;
+  float attention_factor;   /* <= 0: the default amplitude */
+} mla_rope_params;
+typedef struct {
+  int32_t d_r;
+  int32_t layout;
+  float amplitude;
+  int32_t reserved;
+  uint64_t turn[128];       /* f_k / (2 pi) in units of 2^-64 turns per position */
+} mla_rope_table;
+MLA_API int mla_rope_init(const mla_rope_params* params, mla_rope_table* table);
+MLA_API int mla_rope(int32_t dtype, const mla_rope_table* table, int64_t n_tokens, int32_t H,
+                     const void* x, int64_t x_token_stride, int64_t x_head_stride,
+                     const int32_t* pos, void* y, int64_t y_token_stride, int64_t y_head_stride,
+                     int32_t transpose, void* stream);
+
+/* --- page plans: block tables and slot maps of a serving step -----------------------
+ * No counterpart on the pages ([MLA-とは] only names PagedAttention).  Request b
+ * (b < B) holds seqlens[b] cached tokens in the pages of block_table row b and
+ * adds new_lens[b] >= 0 tokens in this step (one for a decode step, a chunk of
+ * its prompt, none).  The pages it needs beyond ceil(seqlens[b] / 64) are taken
+ * off the end of the free list free_pages[0 .. *free_count), in request order,
+ * and written into block_table; then, with the new tokens of all requests in
+ * one list of T places (token i of request b at query_start[b] + i):
+ *   query_start [B+1] int32     prefix sum of new_lens
+ *   positions   [T] int32       seqlens[b] + i
+ *   slots       [T] int64       page * 64 + position % 64
+ *   token_request [T] int32     b (may be NULL)
+ *   seqlens_out [B] int32       seqlens[b] + new_lens[b]
+ *   free_count_out [1] int32    pages left
+ * Places behind the last token get -1 in positions, slots and token_request.
+ * seqlens_out may be seqlens and free_count_out may be free_count (an in-place
+ * step, as in a captured graph); other outputs must not overlap inputs.
+ * free_pages has free_capacity entries and is not changed.  If the step cannot
+ * be served as a whole (more pages needed than are free, more than T tokens, a
+ * sequence past 64 * max_blocks, a negative length or count) nothing is taken:
+ * MLA_ERR_BOUNDS is recorded in the device status word, every place gets -1,
+ * query_start is 0, and lengths, count and block_table stay.  A page id outside
+ * [0, num_pages) gives its tokens slot -1 and records MLA_ERR_BOUNDS.
+ * workspace: mla_plan_pages_workspace_bytes() bytes, zeroed by the caller before
+ * its first use; every call leaves it zero, and calls that may run at the same
+ * time need one each.
+ * mla_release_pages returns the pages of every request with release[b] != 0 to
+ * the end of free_pages (ascending requests and blocks), sets those block_table
+ * entries to -1 and seqlens[b] to 0, and updates free_count in place; if a page
+ * id is outside the pool, a length outside [0, 64 * max_blocks], or free_pages
+ * would overflow, nothing is changed and MLA_ERR_BOUNDS is recorded.  A page
+ * held by two requests must not be released twice. */
+MLA_API size_t mla_plan_pages_workspace_bytes(void);
+MLA_API int mla_plan_pages(int32_t B, const int32_t* seqlens, const int32_t* new_lens,
+                           int32_t* block_table, int32_t max_blocks, const int32_t* free_pages,
+                           int32_t free_capacity, const int32_t* free_count, int64_t num_pages,
+                           int32_t T, int32_t* query_start, int32_t* positions, int64_t* slots,
+                           int32_t* token_request, int32_t* seqlens_out, int32_t* free_count_out,
+                           void* workspace, size_t workspace_bytes, void* stream);
+MLA_API int mla_release_pages(int32_t B, int32_t* seqlens, const int32_t* release,
+                              int32_t* block_table, int32_t max_blocks, int32_t* free_pages,
+                              int32_t free_capacity, int32_t* free_count, int64_t num_pages,
+                              void* stream);
+
+/* --- cache writes of many tokens ---------------------------------------------------
+ * The rows that mla_cache_append writes, for any number of tokens that are
+ * projected already (x = W^DKV h, e.g. a prompt's, by a matrix product):
+ *   row = [x[0:d_c] / sqrt(mean(x[0:d_c]^2) + eps) * gamma || RoPE(x[d_c:d_c+d_r], position)]
+ * x [T rows of d_c + d_r], row t at x + t * x_stride (elements; a slice of a
+ * wider projection is fine), 16-byte aligned rows; gamma [d_c] fp32 or NULL;
+ * table: a rope table with its d_r = dims->d_r, or NULL to store x[d_c:] as it
+ * is.  Of dims only d_c, d_r and dtype are read (and d_r, cache_capacity, B
+ * where named).
+ * mla_cache_write_paged: token t goes to row slots[t] of cache_pool [num_pages, 64,
+ * d_c + d_r] (dtype) with positions[t] as its angle (positions may be NULL with
+ * table NULL).  slots[t] < 0 skips the token; a slot past the pool is skipped
+ * and records MLA_ERR_BOUNDS.  Rows without a slot stay as they are.  Each slot
+ * at most once per call (of two, either row or a mix of both is stored).
+ * MLA_F32 needs d_r % 4 == 0. */
+MLA_API int mla_cache_write_paged(const mla_dims* dims, int32_t T, const void* x,
+                                  int64_t x_stride, const float* gamma, float eps,
+                                  const mla_rope_table* table, const int32_t* positions,
+                                  const int64_t* slots, void* cache_pool, int64_t num_pages,
+                                  void* stream);
+
+/* --- paged 8-bit latent cache --------------------------------------------------------
+ * The 8-bit cache in pages, with one fp32 scale for each page (block of 64
+ * tokens; the latent is the one head all heads share).  cache_pool [num_pages, 64,
+ * d_c + 2 d_r bytes]: row = d_c E4M3 codes (OCP E4M3) then d_r bf16 RoPE keys,
+ * both in units of page_scales[page]:
+ *   c~_j = code_j * scale,   k^R_j = stored_j * scale,
+ *   scale = 2^k, the smallest with max |c| / 2^k <= 448 over the rows of the page
+ *   when it was last written to, never below 2^-40 or above 2^120.
+ * mla_cache_write_fp8_paged writes the rows of query_start[b+1] - query_start[b]
+ * new tokens of each request (x rows query_start[b] ...), the last ones of its
+ * seqlens[b] (the lengths after the step, as mla_plan_pages leaves them), into
+ * the pages of block_table.  A page that held rows before keeps its scale or
+ * gets a larger one; then its earlier rows are rescaled by a power of two (exact
+ * for k^R and for codes that stay normal E4M3 numbers, the others are rounded to
+ * nearest even once more).  Rows behind a sequence's last and pages without new
+ * tokens stay as they are.  No page may be written for two requests in one
+ * call.  A request whose lengths do not fit (negative counts, more than T rows,
+ * seqlens[b] below its count or above cache_capacity) is skipped, a page id
+ * outside the pool skips that page; both record MLA_ERR_BOUNDS.
+ * mla_decode_fp8_paged is mla_decode_paged over the dequantised rows [c~ || k^R]:
+ * same q_cat, seqlens, scale, splits, workspace, partial layout (mla_combine
+ * merges); its default split count never exceeds mla_decode_default_splits.
+ * Shape of both: bf16, d_c = 512, d_r = 64 or 0.  page_scales of pages that are read must
+ * be positive powers of two (as the write leaves them).  Precision: each query
+ * row and the probabilities enter the 8-bit products as sums of two E4M3 terms
+ * (the query exact to 2^-18 of its row's largest value, probabilities to 2^-8),
+ * with fp32 sums; queries must be finite. */
+MLA_API int mla_cache_write_fp8_paged(const mla_dims* dims, int32_t T, const void* x,
+                                      int64_t x_stride, const float* gamma, float eps,
+                                      const mla_rope_table* table, const int32_t* query_start,
+                                      const int32_t* seqlens, const int32_t* block_table,
+                                      int32_t max_blocks, void* cache_pool, float* page_scales,
+                                      int64_t num_pages, void* stream);
+MLA_API int mla_decode_fp8_paged(const mla_dims* dims, const void* q_cat, const void* cache_pool,
+                                 const float* page_scales, int64_t num_pages,
+                                 const int32_t* block_table, int32_t max_blocks,
+                                 const int32_t* seqlens, float softmax_scale, int num_splits,
+                                 void* workspace, size_t workspace_bytes, int* splits_used,
+                                 void* stream);
+
 /* --- 3+4 without a workspace -------------------------------------------------
  * No counterpart on the pages: this is a convenience of this library.
  * For callers that cannot allocate device memory (plugins that only receive

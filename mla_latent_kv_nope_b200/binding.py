@@ -30,7 +30,9 @@ EXPORTED = (
     "mla_merge_partials", "mla_debug_inject_wait", "mla_cache_fp8_row_bytes",
     "mla_cache_append_fp8", "mla_decode_fp8", "mla_fold_output_weights",
     "mla_out_proj_folded_workspace_bytes", "mla_out_proj_folded", "mla_prefill_workspace_bytes",
-    "mla_prefill",
+    "mla_prefill", "mla_rope_init", "mla_rope", "mla_plan_pages_workspace_bytes",
+    "mla_plan_pages", "mla_release_pages", "mla_cache_write_paged", "mla_cache_write_fp8_paged",
+    "mla_decode_fp8_paged",
 )
 
 PAGE_ROWS = 64   # rows per page of a paged latent cache (one decode work tile)
@@ -46,6 +48,20 @@ class CDims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("d_c", ctypes.c_int32),
                 ("d_r", ctypes.c_int32), ("d_nope", ctypes.c_int32), ("d_v", ctypes.c_int32),
                 ("cache_capacity", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class CRopeParams(ctypes.Structure):
+    _fields_ = [("d_r", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("base", ctypes.c_float), ("factor", ctypes.c_float),
+                ("original_len", ctypes.c_float), ("beta_fast", ctypes.c_float),
+                ("beta_slow", ctypes.c_float), ("attention_factor", ctypes.c_float)]
+
+
+class RopeTable(ctypes.Structure):
+    """mla_rope_table: host-side angles of a rotation (see rope_table)."""
+    _fields_ = [("d_r", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("amplitude", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("turn", ctypes.c_uint64 * 128)]
 
 
 @dataclass(frozen=True)
@@ -119,6 +135,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "mla_cache_append_fp8": (ctypes.c_int, [D, I32, P, P, P, F, F, P, P, P, P, SZ, P]),
         "mla_decode_fp8": (ctypes.c_int, [D, P, P, P, P, F, ctypes.c_int, P, SZ,
                                           ctypes.POINTER(ctypes.c_int), P]),
+        "mla_rope_init": (ctypes.c_int, [ctypes.POINTER(CRopeParams), ctypes.POINTER(RopeTable)]),
+        "mla_rope": (ctypes.c_int, [I32, P, I64, I32, P, I64, I64, P, P, I64, I64, I32, P]),
+        "mla_plan_pages_workspace_bytes": (SZ, []),
+        "mla_plan_pages": (ctypes.c_int, [I32, P, P, P, I32, P, I32, P, I64, I32, P, P, P, P, P,
+                                          P, P, SZ, P]),
+        "mla_release_pages": (ctypes.c_int, [I32, P, P, P, I32, P, I32, P, I64, P]),
+        "mla_cache_write_paged": (ctypes.c_int, [D, I32, P, I64, P, F, P, P, P, P, I64, P]),
+        "mla_cache_write_fp8_paged": (ctypes.c_int, [D, I32, P, I64, P, F, P, P, P, P, I32, P, P,
+                                                     I64, P]),
+        "mla_decode_fp8_paged": (ctypes.c_int, [D, P, P, P, I64, P, I32, P, F, ctypes.c_int, P,
+                                                SZ, ctypes.POINTER(ctypes.c_int), P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -439,6 +466,221 @@ def out_proj_folded(dims: Dims, o_lat, W_fold, u, workspace, stream=None):
         ctypes.byref(dims.c()), d_model, _ptr(o_lat), _ptr(W_fold), _ptr(u), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream))
     _check("mla_out_proj_folded", st)
+
+
+# ---------------------------------------------------------------------------
+# Paged serving: rotary positions, page plans, writes of many tokens, 8-bit pages.
+_ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+_ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def _same_device(first, *rest):
+    """The device index all CUDA tensors of a call share."""
+    dev = first.device.index
+    for t in rest:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    return dev
+
+
+def _on(dev, stream, fn, *args):
+    """Call fn(*args, stream) with `dev` current (its current stream unless one is given)."""
+    if torch.cuda.current_device() == dev:
+        return fn(*args, (stream or torch.cuda.current_stream(dev)).cuda_stream)
+    with torch.cuda.device(dev):
+        return fn(*args, (stream or torch.cuda.current_stream(dev)).cuda_stream)
+
+
+def _table_ptr(table):
+    if table is None:
+        return None
+    if not isinstance(table, RopeTable):
+        raise TypeError("table must come from rope_table()")
+    return ctypes.addressof(table)
+
+
+def _need_rows(x, dtype, width, name):
+    """[T, width] rows with unit inner stride (rows of a wider matrix are fine)."""
+    if (not x.is_cuda or x.dtype != dtype or x.dim() != 2 or x.shape[1] != width
+            or (width > 1 and x.stride(1) != 1)):
+        raise ValueError(f"{name}: expected CUDA {dtype} rows [T, {width}] with unit inner "
+                         f"stride, got {x.device} {x.dtype} {tuple(x.shape)} "
+                         f"strides {x.stride()}")
+
+
+def rope_table(d_r: int, base: float = 10000.0, layout: str = "half", scaling: str = "none",
+               factor: float = 1.0, original_len: float = 4096.0, beta_fast: float = 32.0,
+               beta_slow: float = 1.0, attention_factor: float = 0.0) -> RopeTable:
+    """mla_rope_init: the angles of a rotation of d_r values.  layout "half" pairs
+    (x[k], x[k + d_r/2]), "interleaved" (x[2k], x[2k+1]); scaling "none",
+    "linear", "ntk" or "yarn" stretches it by ``factor`` for long contexts."""
+    if layout not in _ROPE_LAYOUT:
+        raise ValueError(f"layout must be one of {sorted(_ROPE_LAYOUT)}, got {layout!r}")
+    if scaling not in _ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALING)}, got {scaling!r}")
+    p = CRopeParams(d_r, _ROPE_LAYOUT[layout], _ROPE_SCALING[scaling], base, factor, original_len,
+                    beta_fast, beta_slow, attention_factor)
+    t = RopeTable()
+    _check("mla_rope_init", load_library().mla_rope_init(ctypes.byref(p), ctypes.byref(t)))
+    return t
+
+
+def rope(table: RopeTable, x, pos, out=None, transpose=False, stream=None):
+    """mla_rope: rotate the rows of x [T, H, d_r] (or [T, d_r]; any token and head
+    strides, e.g. the last d_r of each head of a [T, H, d_nope + d_r] query) by
+    pos [T] int32 into ``out`` (x itself rotates in place; a new contiguous
+    tensor if None).  ``transpose`` applies the transposed rotation (the
+    gradient of the rotation's output taken back to its input)."""
+    tab = _table_ptr(table)
+    if tab is None:
+        raise TypeError("table must come from rope_table()")
+    if (x.dim() not in (2, 3) or x.shape[-1] != table.d_r or not x.is_cuda
+            or x.dtype not in (torch.bfloat16, torch.float32) or x.stride(-1) != 1):
+        raise ValueError(f"x: expected CUDA bf16 or fp32 [T, (H,) {table.d_r}] with unit inner "
+                         f"stride, got {x.device} {x.dtype} {tuple(x.shape)} strides {x.stride()}")
+    T = x.shape[0]
+    _need(pos, torch.int32, (T,), "pos")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype or not out.is_cuda or out.stride(-1) != 1:
+        raise ValueError("out must match x's shape and dtype, with unit inner stride")
+    heads = x.dim() == 3
+    if heads and x.shape[1] == 0:
+        return out
+    dev = _same_device(x, pos, out)
+    st = _on(dev, stream, load_library().mla_rope, MLA_BF16 if x.dtype == torch.bfloat16 else MLA_F32,
+             tab, T, x.shape[1] if heads else 1, x.data_ptr(), x.stride(0),
+             x.stride(1) if heads else 0, _ptr(pos), out.data_ptr(), out.stride(0),
+             out.stride(1) if heads else 0, int(bool(transpose)))
+    _check("mla_rope", st)
+    return out
+
+
+def plan_pages_workspace_bytes() -> int:
+    """Bytes of zeroed workspace plan_pages needs."""
+    return int(load_library().mla_plan_pages_workspace_bytes())
+
+
+def plan_pages(seqlens, new_lens, block_table, free_pages, free_count, num_pages, query_start,
+               positions, slots, seqlens_out, free_count_out, workspace, token_request=None,
+               stream=None):
+    """mla_plan_pages: take the pages this step's new tokens need off the free
+    list into block_table [B, max_blocks], and fill query_start [B+1],
+    positions [T] (int32) and slots [T] (int64); seqlens_out and
+    free_count_out may be seqlens and free_count."""
+    B, T = seqlens.shape[0], positions.shape[0]
+    i32 = torch.int32
+    _need(seqlens, i32, (B,), "seqlens")
+    _need(new_lens, i32, (B,), "new_lens")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    _need(block_table, i32, (B, block_table.shape[1]), "block_table")
+    _need(free_pages, i32, (free_pages.numel(),), "free_pages")
+    _need(free_count, i32, (1,), "free_count")
+    _need(query_start, i32, (B + 1,), "query_start")
+    _need(positions, i32, (T,), "positions")
+    _need(slots, torch.int64, (T,), "slots")
+    _need(seqlens_out, i32, (B,), "seqlens_out")
+    _need(free_count_out, i32, (1,), "free_count_out")
+    if token_request is not None:
+        _need(token_request, i32, (T,), "token_request")
+    _need_ws(workspace)
+    dev = _same_device(seqlens, new_lens, block_table, free_pages, free_count, query_start,
+                       positions, slots, seqlens_out, free_count_out, workspace, token_request)
+    st = _on(dev, stream, load_library().mla_plan_pages, B, _ptr(seqlens), _ptr(new_lens),
+             _ptr(block_table), block_table.shape[1], _ptr(free_pages), free_pages.shape[0],
+             _ptr(free_count), num_pages, T, _ptr(query_start), _ptr(positions), _ptr(slots),
+             _ptr(token_request), _ptr(seqlens_out), _ptr(free_count_out), _ptr(workspace),
+             workspace.numel() * workspace.element_size())
+    _check("mla_plan_pages", st)
+
+
+def release_pages(seqlens, release, block_table, free_pages, free_count, num_pages, stream=None):
+    """mla_release_pages: return the pages of every request with release[b] != 0 to
+    the free list (seqlens, block_table, free_pages and free_count in place)."""
+    B = seqlens.shape[0]
+    i32 = torch.int32
+    _need(seqlens, i32, (B,), "seqlens")
+    _need(release, i32, (B,), "release")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    _need(block_table, i32, (B, block_table.shape[1]), "block_table")
+    _need(free_pages, i32, (free_pages.numel(),), "free_pages")
+    _need(free_count, i32, (1,), "free_count")
+    dev = _same_device(seqlens, release, block_table, free_pages, free_count)
+    st = _on(dev, stream, load_library().mla_release_pages, B, _ptr(seqlens), _ptr(release),
+             _ptr(block_table), block_table.shape[1], _ptr(free_pages), free_pages.shape[0],
+             _ptr(free_count), num_pages)
+    _check("mla_release_pages", st)
+
+
+def cache_write_paged(dims: Dims, x, gamma, positions, slots, cache_pool, table=None, eps=1e-6,
+                      stream=None):
+    """mla_cache_write_paged: the rows [RMSNorm(x_c) * gamma || RoPE(x_r, position)] of
+    projected tokens x [T, d_c + d_r] to rows ``slots`` (int64, -1: none) of
+    cache_pool [num_pages, 64, d_c + d_r].  Without a table x_r is stored as it is."""
+    dt, T = dims.torch_dtype, x.shape[0]
+    _need_rows(x, dt, dims.R, "x")
+    _need(slots, torch.int64, (T,), "slots")
+    if positions is not None:
+        _need(positions, torch.int32, (T,), "positions")
+    if gamma is not None:
+        _need(gamma, torch.float32, (dims.d_c,), "gamma")
+    _need(cache_pool, dt, (cache_pool.shape[0], PAGE_ROWS, dims.R), "cache_pool")
+    dev = _same_device(x, slots, positions, gamma, cache_pool)
+    st = _on(dev, stream, load_library().mla_cache_write_paged, ctypes.byref(dims.c()), T,
+             x.data_ptr(), x.stride(0) if T > 1 else dims.R, _ptr(gamma), eps, _table_ptr(table),
+             _ptr(positions), _ptr(slots), _ptr(cache_pool), cache_pool.shape[0])
+    _check("mla_cache_write_paged", st)
+
+
+def _need_fp8_pages(dims: Dims, pool, page_scales, block_table):
+    n = pool.shape[0]
+    _need(pool, torch.uint8, (n, PAGE_ROWS, dims.d_c + 2 * dims.d_r), "cache_pool")
+    _need(page_scales, torch.float32, (n,), "page_scales")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    _need(block_table, torch.int32, (dims.B, block_table.shape[1]), "block_table")
+
+
+def cache_write_fp8_paged(dims: Dims, x, gamma, query_start, seqlens, block_table, cache_pool,
+                          page_scales, table=None, eps=1e-6, stream=None):
+    """mla_cache_write_fp8_paged: the rows of cache_write_paged into an 8-bit pool
+    [num_pages, 64, d_c + 2 d_r] uint8 with one scale per page [num_pages];
+    request b's rows are x[query_start[b]:query_start[b+1]], the last of its
+    seqlens[b] tokens (the lengths after the step)."""
+    T = x.shape[0]
+    _need_rows(x, dims.torch_dtype, dims.R, "x")
+    _need(query_start, torch.int32, (dims.B + 1,), "query_start")
+    _need(seqlens, torch.int32, (dims.B,), "seqlens")
+    if gamma is not None:
+        _need(gamma, torch.float32, (dims.d_c,), "gamma")
+    _need_fp8_pages(dims, cache_pool, page_scales, block_table)
+    dev = _same_device(x, gamma, query_start, seqlens, block_table, cache_pool, page_scales)
+    st = _on(dev, stream, load_library().mla_cache_write_fp8_paged, ctypes.byref(dims.c()), T,
+             x.data_ptr(), x.stride(0) if T > 1 else dims.R, _ptr(gamma), eps, _table_ptr(table),
+             _ptr(query_start), _ptr(seqlens), _ptr(block_table), block_table.shape[1],
+             _ptr(cache_pool), _ptr(page_scales), cache_pool.shape[0])
+    _check("mla_cache_write_fp8_paged", st)
+
+
+def decode_fp8_paged(dims: Dims, q_cat, cache_pool, page_scales, block_table, seqlens,
+                     softmax_scale, workspace, num_splits=0, stream=None) -> int:
+    """mla_decode_fp8_paged: mla_decode over an 8-bit paged cache (see
+    cache_write_fp8_paged); returns the splits used, for combine."""
+    _need(q_cat, dims.torch_dtype, (dims.B, dims.H, dims.R), "q_cat")
+    _need_fp8_pages(dims, cache_pool, page_scales, block_table)
+    _need(seqlens, torch.int32, (dims.B,), "seqlens")
+    _need_ws(workspace)
+    used = ctypes.c_int(0)
+    dev = _same_device(q_cat, cache_pool, page_scales, block_table, seqlens, workspace)
+    st = _on(dev, stream, load_library().mla_decode_fp8_paged, ctypes.byref(dims.c()),
+             _ptr(q_cat), _ptr(cache_pool), _ptr(page_scales), cache_pool.shape[0],
+             _ptr(block_table), block_table.shape[1], _ptr(seqlens), float(softmax_scale),
+             num_splits, _ptr(workspace), workspace.numel() * workspace.element_size(),
+             ctypes.byref(used))
+    _check("mla_decode_fp8_paged", st)
+    return used.value
 
 
 def get_device_status(stream=None) -> int:

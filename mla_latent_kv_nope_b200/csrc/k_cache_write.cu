@@ -1,0 +1,376 @@
+// Latent rows of many new tokens into a paged cache: the row
+//   [RMSNorm(x[0:d_c]) * gamma || RoPE(x[d_c:], position)]
+// of each projected token x = W^DKV h, stored in the cache dtype at its slot, or
+// as E4M3 codes with one power-of-two scale per page.
+#include <cuda_fp8.h>
+
+#include "kernels.h"
+#include "rope_table.cuh"
+
+namespace mla {
+
+namespace {
+
+template <typename T, int kVec>
+__device__ __forceinline__ void unpack16(const uint4& v, float (&f)[kVec]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+}
+template <typename T, int kVec>
+__device__ __forceinline__ uint4 pack16(const float (&f)[kVec]) {
+  uint32_t w[4];
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(f[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void load_gamma(const float* gamma, int c, int n, float* g) {
+#pragma unroll
+  for (int i = 0; i < n; i += 4) {
+    const float4 v = gamma ? *reinterpret_cast<const float4*>(gamma + c + i)
+                           : make_float4(1.f, 1.f, 1.f, 1.f);
+    g[i] = v.x, g[i + 1] = v.y, g[i + 2] = v.z, g[i + 3] = v.w;
+  }
+}
+
+// The two places of pair k of a d_r-wide rotary block.
+__device__ __forceinline__ void pair_at(const mla_rope_table& tab, int d_r, int k, int* i, int* j) {
+  const bool inter = tab.layout == MLA_ROPE_INTERLEAVED;
+  *i = inter ? 2 * k : k;
+  *j = inter ? 2 * k + 1 : k + d_r / 2;
+}
+
+// ---------------------------------------------------------------- 16- and 32-bit pages
+// One warp per token: the row is read once with 16-byte loads and stays in
+// registers (kUnits 16-byte units per lane), the sum of squares is a warp
+// reduction, and the row goes out with 16-byte stores.  Bound by HBM (one read
+// and one write of the row), for a decode step by latency.
+constexpr int kWriteWarps = 4;
+
+template <typename T, int kUnits>
+__global__ void __launch_bounds__(32 * kWriteWarps)
+cache_write_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
+                   const T* __restrict__ x, int64_t x_stride, const float* __restrict__ gamma,
+                   float eps, const int32_t* __restrict__ positions,
+                   const int64_t* __restrict__ slots, int T_rows, int d_c, int d_r,
+                   int64_t total_rows, T* __restrict__ pool, int* __restrict__ status) {
+  constexpr int kVec = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31;
+  const int64_t t = int64_t(blockIdx.x) * kWriteWarps + (threadIdx.x >> 5);
+  if (t >= T_rows) return;
+  pdl_wait();
+  const T* row = x + t * x_stride;
+  uint4 v[kUnits];
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    const int c = (lane + 32 * u) * kVec;
+    v[u] = c < d_c ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+  }
+  const int64_t slot = slots[t];
+  if (slot < 0) return;               // padding
+  if (slot >= total_rows) {
+    if (lane == 0) record_status(status, MLA_ERR_BOUNDS);
+    return;
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    float f[kVec];
+    unpack16<T, kVec>(v[u], f);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) ss = fmaf(f[i], f[i], ss);
+  }
+  const float inv = 1.f / sqrtf(warp_sum(ss) / float(d_c) + eps);
+  T* dst = pool + slot * (d_c + d_r);
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    const int c = (lane + 32 * u) * kVec;
+    if (c < d_c) {
+      float f[kVec], g[kVec];
+      unpack16<T, kVec>(v[u], f);
+      load_gamma(gamma, c, kVec, g);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) f[i] = f[i] * inv * g[i];
+      *reinterpret_cast<uint4*>(dst + c) = pack16<T, kVec>(f);
+    }
+  }
+  const int64_t pos = rotate ? positions[t] : 0;
+  for (int k = lane; k < d_r / 2; k += 32) {
+    int i = k, j = k + d_r / 2;
+    float c = 1.f, s = 0.f;
+    if (rotate) {
+      pair_at(tab, d_r, k, &i, &j);
+      rope_turn_cos_sin(tab.turn[k], pos, tab.amplitude, &c, &s);
+    }
+    const float a = Storage<T>::to_f(row[d_c + i]), b = Storage<T>::to_f(row[d_c + j]);
+    dst[d_c + i] = Storage<T>::from_f(rotate ? a * c - b * s : a);
+    dst[d_c + j] = Storage<T>::from_f(rotate ? a * s + b * c : b);
+  }
+}
+
+// ---------------------------------------------------------------- 8-bit pages
+// One block per (request, page that its new tokens touch), at most 64 rows.
+// Each warp keeps its rows in registers (one read of x), the page's largest
+// magnitude is reduced over the block, the new exponent fixed, and the codes
+// written.  If the page held rows before and its scale grows, those rows are
+// rescaled first by a power of two, which is exact for the rotary keys and for
+// codes that stay normal E4M3 values and rounds the others once more.
+constexpr int k8Threads = 512;
+constexpr int k8Warps = k8Threads / 32;
+constexpr int k8Rows = kTileKeys / k8Warps;   // rows per warp
+constexpr int k8Dc = 512;
+constexpr int kMinScaleExp = -40, kMaxScaleExp = 120;
+
+// Smallest k with amax <= 448 * 2^k, within the limits (448 = 0.875 * 2^9).
+__device__ __forceinline__ int scale_exponent(float amax) {
+  if (!(amax > 0.f)) return kMinScaleExp;
+  int e;
+  const float f = frexpf(amax, &e);
+  const int k = f <= 0.875f ? e - 9 : e - 8;
+  return min(max(k, kMinScaleExp), kMaxScaleExp);
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+__device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float f) {
+  const __half2 lo(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w & 0xFFFFu), __NV_E4M3));
+  const __half2 hi(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w >> 16), __NV_E4M3));
+  return e4m3x4(__low2float(lo) * f, __high2float(lo) * f, __low2float(hi) * f,
+                __high2float(hi) * f);
+}
+
+template <int kDr>
+__global__ void __launch_bounds__(k8Threads)
+cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
+                    const __nv_bfloat16* __restrict__ x, int64_t x_stride, int T_rows,
+                    const float* __restrict__ gamma, float eps,
+                    const int32_t* __restrict__ query_start, const int32_t* __restrict__ seqlens,
+                    int B, int64_t cap, const PageMap pm, uint8_t* __restrict__ pool,
+                    float* __restrict__ page_scales, int* __restrict__ status) {
+  constexpr int kRowBytes = k8Dc + 2 * kDr;
+  __shared__ int s_scan[k8Warps];
+  __shared__ int s_req, s_first, s_total;
+  __shared__ float s_max[k8Warps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+
+  // The request whose pages cover this block's index: requests are counted
+  // blockDim at a time, until the one that passes it.
+  int base = 0;
+  const int task = blockIdx.x;
+  if (tid == 0) s_req = -1;
+  __syncthreads();
+  for (int b0 = 0; b0 < B; b0 += k8Threads) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < B) {
+      const int32_t q0 = query_start[b], q1 = query_start[b + 1], L = seqlens[b];
+      const int64_t add = int64_t(q1) - q0;
+      if (add < 0 || q0 < 0 || q1 > T_rows || (add > 0 && (L < add || L > cap))) {
+        record_status(status, MLA_ERR_BOUNDS);
+      } else if (add > 0) {
+        n = int((int64_t(L) - 1) / kTileKeys - (L - add) / kTileKeys) + 1;
+      }
+    }
+    int e = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, e, o);
+      if (lane >= o) e += u;
+    }
+    if (lane == 31) s_scan[warp] = e;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < k8Warps; ++w)
+      if (w < warp) e += s_scan[w];
+    e += base;
+    if (task < e && task >= e - n) s_req = b, s_first = e - n;
+    if (tid == k8Threads - 1) s_total = e;
+    __syncthreads();
+    if (s_req >= 0) break;
+    base = s_total;
+  }
+  const int b = s_req;
+  if (b < 0) return;
+  const int64_t q0 = query_start[b], end = seqlens[b];
+  const int64_t start = end - (query_start[b + 1] - q0);        // first new position
+  const int64_t j = start / kTileKeys + (task - s_first);       // this page's block
+  const int64_t first = pm.tile_row(b, j);
+  if (first < 0) {
+    if (tid == 0) record_status(status, MLA_ERR_BOUNDS);
+    return;
+  }
+  const int r0 = int(max(start - j * kTileKeys, int64_t(0)));                    // new rows
+  const int r1 = int(min(end - j * kTileKeys, int64_t(kTileKeys)));              // [r0, r1)
+  const int64_t x0 = q0 + j * kTileKeys - start;                                 // x row of page row 0
+  uint8_t* page = pool + first * kRowBytes;
+  float* page_scale = page_scales + first / kTileKeys;
+  const float old_scale = r0 ? *page_scale : 0.f;
+
+  // Rows r0 + warp, r0 + warp + 16, ... of the page: 16 values of each per lane.
+  uint4 v[k8Rows][2];
+  float p1[k8Rows], p2[k8Rows];
+#pragma unroll
+  for (int i = 0; i < k8Rows; ++i) {
+    const int r = r0 + warp + i * k8Warps;
+    if (r < r1) {
+      const __nv_bfloat16* row = x + (x0 + r) * x_stride;
+      v[i][0] = reinterpret_cast<const uint4*>(row)[lane];
+      v[i][1] = reinterpret_cast<const uint4*>(row)[lane + 32];
+      if constexpr (kDr > 0) {
+        int a = lane, c = lane + kDr / 2;
+        if (rotate) pair_at(tab, kDr, lane, &a, &c);
+        p1[i] = __bfloat162float(row[k8Dc + a]);
+        p2[i] = __bfloat162float(row[k8Dc + c]);
+      }
+    } else {
+      v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
+      p1[i] = p2[i] = 0.f;
+    }
+  }
+  float g[16];
+  load_gamma(gamma, lane * 8, 8, g);
+  load_gamma(gamma, 256 + lane * 8, 8, g + 8);
+  float inv[k8Rows], amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < k8Rows; ++i) {
+    float f[16], ss = 0.f;
+    unpack16<__nv_bfloat16, 8>(v[i][0], *reinterpret_cast<float(*)[8]>(f));
+    unpack16<__nv_bfloat16, 8>(v[i][1], *reinterpret_cast<float(*)[8]>(f + 8));
+#pragma unroll
+    for (int e = 0; e < 16; ++e) ss = fmaf(f[e], f[e], ss);
+    inv[i] = 1.f / sqrtf(warp_sum(ss) / float(k8Dc) + eps);
+    if (r0 + warp + i * k8Warps < r1) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(f[e] * inv[i] * g[e]));
+    }
+  }
+  amax = warp_max(amax);
+  if (lane == 0) s_max[warp] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < k8Warps; ++w) amax = fmaxf(amax, s_max[w]);
+  int k = scale_exponent(amax);
+  if (r0 && old_scale > 0.f && old_scale < INFINITY) {
+    int e;
+    const float f = frexpf(old_scale, &e);
+    k = max(k, min(f > 0.5f ? e : e - 1, kMaxScaleExp));
+    const float ratio = old_scale * ldexpf(1.f, -k);
+    if (ratio != 1.f)
+      for (int r = warp; r < r0; r += k8Warps) {
+        uint4* row = reinterpret_cast<uint4*>(page + r * kRowBytes);
+        uint4 c = row[lane];
+        c.x = rescale_e4m3x4(c.x, ratio);
+        c.y = rescale_e4m3x4(c.y, ratio);
+        c.z = rescale_e4m3x4(c.z, ratio);
+        c.w = rescale_e4m3x4(c.w, ratio);
+        row[lane] = c;
+        if (kDr > 0 && lane < kDr / 8) {
+          float f8[8];
+          unpack16<__nv_bfloat16, 8>(row[32 + lane], f8);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) f8[q] *= ratio;
+          row[32 + lane] = pack16<__nv_bfloat16, 8>(f8);
+        }
+      }
+  }
+  const float inv_scale = ldexpf(1.f, -k);
+  if (tid == 0) *page_scale = ldexpf(1.f, k);
+#pragma unroll
+  for (int i = 0; i < k8Rows; ++i) {
+    const int r = r0 + warp + i * k8Warps;
+    if (r >= r1) continue;
+    uint8_t* row = page + r * kRowBytes;
+    float f[16];
+    unpack16<__nv_bfloat16, 8>(v[i][0], *reinterpret_cast<float(*)[8]>(f));
+    unpack16<__nv_bfloat16, 8>(v[i][1], *reinterpret_cast<float(*)[8]>(f + 8));
+#pragma unroll
+    for (int e = 0; e < 16; ++e) f[e] = f[e] * inv[i] * g[e] * inv_scale;
+    reinterpret_cast<uint2*>(row)[lane] =
+        make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+    reinterpret_cast<uint2*>(row)[lane + 32] =
+        make_uint2(e4m3x4(f[8], f[9], f[10], f[11]), e4m3x4(f[12], f[13], f[14], f[15]));
+    if constexpr (kDr > 0) {
+      int a = lane, c = lane + kDr / 2;
+      float y1 = p1[i], y2 = p2[i];
+      if (rotate) {
+        pair_at(tab, kDr, lane, &a, &c);
+        float cs, sn;
+        rope_turn_cos_sin(tab.turn[lane], j * kTileKeys + r, tab.amplitude, &cs, &sn);
+        y1 = p1[i] * cs - p2[i] * sn;
+        y2 = p1[i] * sn + p2[i] * cs;
+      }
+      // Rounded to bf16 as in a bf16 cache; the power of two is exact.
+      __nv_bfloat16* rope = reinterpret_cast<__nv_bfloat16*>(row + k8Dc);
+      rope[a] = __float2bfloat16_rn(__bfloat162float(__float2bfloat16_rn(y1)) * inv_scale);
+      rope[c] = __float2bfloat16_rn(__bfloat162float(__float2bfloat16_rn(y2)) * inv_scale);
+    }
+  }
+}
+
+}  // namespace
+
+template <typename T>
+cudaError_t launch_cache_write(const mla_rope_table* tab, const T* x, int64_t x_stride,
+                               const float* gamma, float eps, const int32_t* positions,
+                               const int64_t* slots, int T_rows, int d_c, int d_r,
+                               int64_t total_rows, T* pool, int* status, cudaStream_t stream) {
+  const dim3 grid((T_rows + kWriteWarps - 1) / kWriteWarps), block(32 * kWriteWarps);
+  const mla_rope_table t = tab ? *tab : mla_rope_table{};
+  const int units = (d_c * int(sizeof(T)) / 16 + 31) / 32;   // 16-byte units per lane
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, grid, block, 0, stream, t, int(tab != nullptr), x, x_stride, gamma,
+                      eps, positions, slots, T_rows, d_c, d_r, total_rows, pool, status);
+  };
+  if (units <= 1) return go(cache_write_kernel<T, 1>);
+  if (units <= 2) return go(cache_write_kernel<T, 2>);
+  if (units <= 4) return go(cache_write_kernel<T, 4>);
+  return go(cache_write_kernel<T, 8>);
+}
+
+template cudaError_t launch_cache_write<float>(const mla_rope_table*, const float*, int64_t,
+                                               const float*, float, const int32_t*,
+                                               const int64_t*, int, int, int, int64_t, float*,
+                                               int*, cudaStream_t);
+template cudaError_t launch_cache_write<__nv_bfloat16>(const mla_rope_table*, const __nv_bfloat16*,
+                                                       int64_t, const float*, float,
+                                                       const int32_t*, const int64_t*, int, int,
+                                                       int, int64_t, __nv_bfloat16*, int*,
+                                                       cudaStream_t);
+
+cudaError_t launch_cache_write_fp8(const mla_rope_table* tab, const __nv_bfloat16* x,
+                                   int64_t x_stride, int T_rows, const float* gamma, float eps,
+                                   const int32_t* query_start, const int32_t* seqlens, int B,
+                                   int64_t cap, int d_r, const PageMap& pm, uint8_t* pool,
+                                   float* page_scales, int* status, cudaStream_t stream) {
+  const mla_rope_table t = tab ? *tab : mla_rope_table{};
+  // A request with n new tokens touches at most min(n, n / 64 + 2) pages.
+  const int64_t most = int64_t(T_rows) / kTileKeys + 2 * int64_t(B);
+  const dim3 grid(unsigned(most < T_rows ? most : T_rows));
+  auto kernel = d_r ? cache_write8_kernel<64> : cache_write8_kernel<0>;
+  return launch_pdl(kernel, grid, dim3(k8Threads), 0, stream, t, int(tab != nullptr), x, x_stride,
+                    T_rows, gamma, eps, query_start, seqlens, B, cap, pm, pool, page_scales,
+                    status);
+}
+
+}  // namespace mla

@@ -119,4 +119,46 @@ cudaError_t launch_prefill(const __nv_bfloat16* q_nope, const __nv_bfloat16* q_p
                            int H, int d_r, float scale, float rope_base, __nv_bfloat16* out,
                            float* lse, void* workspace, int* status, cudaStream_t stream);
 
+// Rotary positions over strided rows (see mla_rope).
+template <typename T>
+cudaError_t launch_rope(const mla_rope_table& tab, int64_t n_tokens, int H, const T* x, int64_t xt,
+                        int64_t xh, const int32_t* pos, T* y, int64_t yt, int64_t yh,
+                        int transpose, cudaStream_t stream);
+
+// Page plans (see mla_plan_pages, mla_release_pages).  The workspace is one
+// zeroed 32-bit ticket.
+cudaError_t launch_page_plan(const int32_t* seqlens, const int32_t* new_lens, int B,
+                             int32_t* block_table, int max_blocks, const int32_t* free_pages,
+                             int free_capacity, const int32_t* free_count, int64_t num_pages,
+                             int T, int32_t* query_start, int32_t* positions, int64_t* slots,
+                             int32_t* token_request, int32_t* seqlens_out,
+                             int32_t* free_count_out, void* workspace, int* status,
+                             cudaStream_t stream);
+cudaError_t launch_page_release(int32_t* seqlens, const int32_t* release, int B,
+                                int32_t* block_table, int max_blocks, int32_t* free_pages,
+                                int free_capacity, int32_t* free_count, int64_t num_pages,
+                                int* status, cudaStream_t stream);
+
+// Latent rows of T projected tokens into pages (see mla_cache_write_paged and
+// mla_cache_write_fp8_paged); `tab` is null for rows that are rotated already.
+template <typename T>
+cudaError_t launch_cache_write(const mla_rope_table* tab, const T* x, int64_t x_stride,
+                               const float* gamma, float eps, const int32_t* positions,
+                               const int64_t* slots, int T_rows, int d_c, int d_r,
+                               int64_t total_rows, T* pool, int* status, cudaStream_t stream);
+cudaError_t launch_cache_write_fp8(const mla_rope_table* tab, const __nv_bfloat16* x,
+                                   int64_t x_stride, int T_rows, const float* gamma, float eps,
+                                   const int32_t* query_start, const int32_t* seqlens, int B,
+                                   int64_t cap, int d_r, const PageMap& pm, uint8_t* pool,
+                                   float* page_scales, int* status, cudaStream_t stream);
+
+// Decode over a paged 8-bit cache with one scale per page (d_c = 512, d_r = 64
+// or 0), and its default split count on a device of `sms` SMs.
+int decode_fp8_paged_splits(int sms, int H);
+cudaError_t launch_decode_fp8_paged(const __nv_bfloat16* q_cat, const uint8_t* pool,
+                                    const float* page_scales, const PageMap& pm,
+                                    const int32_t* seqlens, int B, int H, int d_r, int64_t cap,
+                                    float scale, int W, float* o_part, float* lse_part,
+                                    int* status, uint64_t inject_wait, cudaStream_t stream);
+
 }  // namespace mla

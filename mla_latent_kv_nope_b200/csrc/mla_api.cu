@@ -408,6 +408,245 @@ int mla_decode_fp8(const mla_dims* d, const void* q_cat, const void* cache, cons
 }
 
 // ---------------------------------------------------------------------------
+// Rotary positions.
+int mla_rope_init(const mla_rope_params* p, mla_rope_table* table) {
+  if (!p || !table) return MLA_ERR_INVALID_ARG;
+  const int d = p->d_r;
+  if (d < 2 || d > 256 || d % 2 || (p->layout != MLA_ROPE_HALF && p->layout != MLA_ROPE_INTERLEAVED) ||
+      p->scaling < MLA_ROPE_UNSCALED || p->scaling > MLA_ROPE_YARN || !(p->base > 1.f) ||
+      !std::isfinite(p->base) || !std::isfinite(p->attention_factor))
+    return MLA_ERR_INVALID_ARG;
+  const bool scaled = p->scaling != MLA_ROPE_UNSCALED;
+  if (scaled && (!(p->factor >= 1.f) || !std::isfinite(p->factor))) return MLA_ERR_INVALID_ARG;
+  const double kPi = 3.14159265358979323846;
+  double base = p->base, low = 0, high = 0;
+  const double factor = scaled ? double(p->factor) : 1.0;
+  if (p->scaling == MLA_ROPE_NTK) {
+    if (d <= 2) return MLA_ERR_INVALID_ARG;
+    base *= pow(factor, double(d) / (d - 2));
+  }
+  if (p->scaling == MLA_ROPE_YARN) {
+    if (!(p->original_len > 0.f) || !std::isfinite(p->original_len) || !(p->beta_slow > 0.f) ||
+        !(p->beta_fast > p->beta_slow) || !std::isfinite(p->beta_fast))
+      return MLA_ERR_INVALID_ARG;
+    const double per = d / (2 * log(base));
+    low = fmax(floor(per * log(p->original_len / (2 * kPi * p->beta_fast))), 0.0);
+    high = fmin(ceil(per * log(p->original_len / (2 * kPi * p->beta_slow))), double(d - 1));
+  }
+  table->d_r = d;
+  table->layout = p->layout;
+  table->reserved = 0;
+  table->amplitude = p->attention_factor > 0.f ? p->attention_factor
+                     : p->scaling == MLA_ROPE_YARN ? float(0.1 * log(factor) + 1.0) : 1.f;
+  for (int k = 0; k < 128; ++k) {
+    double f = 0;
+    if (k < d / 2) {
+      f = pow(base, -2.0 * k / d);
+      if (p->scaling == MLA_ROPE_LINEAR) f /= factor;
+      if (p->scaling == MLA_ROPE_YARN) {
+        const double g = fmin(fmax((k - low) / fmax(high - low, 1e-3), 0.0), 1.0);
+        f = f * (1 - g) + f / factor * g;
+      }
+    }
+    // f <= 1 rad, so the fraction is below 0.16 turns and fits 64 bits.
+    table->turn[k] = uint64_t(f / (2 * kPi) * 18446744073709551616.0);
+  }
+  return MLA_OK;
+}
+
+namespace {
+bool good_table(const mla_rope_table* t) {
+  return t->d_r >= 2 && t->d_r <= 256 && t->d_r % 2 == 0 &&
+         (t->layout == MLA_ROPE_HALF || t->layout == MLA_ROPE_INTERLEAVED);
+}
+inline bool aligned_to(const void* p, size_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+}  // namespace
+
+int mla_rope(int32_t dtype, const mla_rope_table* table, int64_t n_tokens, int32_t H,
+             const void* x, int64_t x_token_stride, int64_t x_head_stride, const int32_t* pos,
+             void* y, int64_t y_token_stride, int64_t y_head_stride, int32_t transpose,
+             void* stream) {
+  if (!table || !good_table(table) || n_tokens < 0 || H <= 0 ||
+      (dtype != MLA_BF16 && dtype != MLA_F32))
+    return MLA_ERR_INVALID_ARG;
+  if (n_tokens >= (int64_t(1) << 31) || H > 65535) return MLA_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return MLA_OK;
+  if (!x || !y || !pos) return MLA_ERR_INVALID_ARG;
+  // Rows of y that overlap would be written twice.
+  const int64_t d = table->d_r, yt = y_token_stride < 0 ? -y_token_stride : y_token_stride,
+                yh = y_head_stride < 0 ? -y_head_stride : y_head_stride;
+  if ((n_tokens > 1 && yt < d) || (H > 1 && yh < d)) return MLA_ERR_INVALID_ARG;
+  const size_t elem = dtype == MLA_BF16 ? 2 : 4;
+  if (!aligned_to(x, elem) || !aligned_to(y, elem) || !aligned_to(pos, 4)) return MLA_ERR_ALIGNMENT;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == MLA_BF16)
+    return cuda_status(launch_rope<__nv_bfloat16>(
+        *table, n_tokens, H, static_cast<const __nv_bfloat16*>(x), x_token_stride, x_head_stride,
+        pos, static_cast<__nv_bfloat16*>(y), y_token_stride, y_head_stride, transpose != 0, s));
+  return cuda_status(launch_rope<float>(*table, n_tokens, H, static_cast<const float*>(x),
+                                        x_token_stride, x_head_stride, pos, static_cast<float*>(y),
+                                        y_token_stride, y_head_stride, transpose != 0, s));
+}
+
+// ---------------------------------------------------------------------------
+// Page plans.
+namespace {
+int check_page_list(int32_t B, int32_t max_blocks, int32_t free_capacity, int64_t num_pages) {
+  if (B <= 0 || max_blocks <= 0 || free_capacity < 0 || num_pages <= 0) return MLA_ERR_INVALID_ARG;
+  if (B > 65535 || num_pages * kTileKeys >= (int64_t(1) << 31) ||
+      int64_t(max_blocks) * kTileKeys >= (int64_t(1) << 31))
+    return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+}  // namespace
+
+size_t mla_plan_pages_workspace_bytes(void) { return 256; }
+
+int mla_plan_pages(int32_t B, const int32_t* seqlens, const int32_t* new_lens,
+                   int32_t* block_table, int32_t max_blocks, const int32_t* free_pages,
+                   int32_t free_capacity, const int32_t* free_count, int64_t num_pages, int32_t T,
+                   int32_t* query_start, int32_t* positions, int64_t* slots,
+                   int32_t* token_request, int32_t* seqlens_out, int32_t* free_count_out,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_page_list(B, max_blocks, free_capacity, num_pages);
+  if (st) return st;
+  if (T < 0 || !seqlens || !new_lens || !block_table || (free_capacity && !free_pages) ||
+      !free_count || !query_start || (T && (!positions || !slots)) || !seqlens_out ||
+      !free_count_out)
+    return MLA_ERR_INVALID_ARG;
+  if (T > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+  const void* i32[] = {seqlens, new_lens, block_table, free_pages, free_count, query_start,
+                       positions, token_request, seqlens_out, free_count_out, workspace};
+  for (const void* p : i32)
+    if (!aligned_to(p, 4)) return MLA_ERR_ALIGNMENT;
+  if (!aligned_to(slots, 8)) return MLA_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < mla_plan_pages_workspace_bytes()) return MLA_ERR_WORKSPACE;
+  return cuda_status(launch_page_plan(seqlens, new_lens, B, block_table, max_blocks, free_pages,
+                                      free_capacity, free_count, num_pages, T, query_start,
+                                      positions, slots, token_request, seqlens_out,
+                                      free_count_out, workspace, status_ptr(),
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+int mla_release_pages(int32_t B, int32_t* seqlens, const int32_t* release, int32_t* block_table,
+                      int32_t max_blocks, int32_t* free_pages, int32_t free_capacity,
+                      int32_t* free_count, int64_t num_pages, void* stream) {
+  int st = check_page_list(B, max_blocks, free_capacity, num_pages);
+  if (st) return st;
+  if (!seqlens || !release || !block_table || (free_capacity && !free_pages) || !free_count)
+    return MLA_ERR_INVALID_ARG;
+  const void* i32[] = {seqlens, release, block_table, free_pages, free_count};
+  for (const void* p : i32)
+    if (!aligned_to(p, 4)) return MLA_ERR_ALIGNMENT;
+  return cuda_status(launch_page_release(seqlens, release, B, block_table, max_blocks, free_pages,
+                                         free_capacity, free_count, num_pages, status_ptr(),
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// Cache writes of many tokens, and the paged 8-bit cache.
+namespace {
+int check_write(const mla_dims* d, int32_t T, const void* x, int64_t x_stride, const float* gamma,
+                float eps, const mla_rope_table* table, const void* cache_pool, int64_t num_pages) {
+  int st = check_dims(d);
+  if (st) return st;
+  if (T < 0 || num_pages <= 0 || !(eps >= 0.f) || x_stride < d->d_c + d->d_r)
+    return MLA_ERR_INVALID_ARG;
+  if (table && (!good_table(table) || table->d_r != d->d_r)) return MLA_ERR_INVALID_ARG;
+  if (num_pages * kTileKeys >= (int64_t(1) << 31)) return MLA_ERR_UNSUPPORTED;
+  if (T && (!x || !cache_pool)) return MLA_ERR_INVALID_ARG;
+  const int64_t elem = d->dtype == MLA_BF16 ? 2 : 4;
+  if ((d->d_c + d->d_r) * elem % 16) return MLA_ERR_UNSUPPORTED;   // fp32 rows with d_r % 4 == 2
+  if (!aligned16(x) || (x_stride * elem) % 16 || !aligned16(gamma) || !aligned16(cache_pool))
+    return MLA_ERR_ALIGNMENT;
+  return MLA_OK;
+}
+int check_fp8_paged(const mla_dims* d) {
+  if (d->dtype != MLA_BF16 || d->d_c != 512 || (d->d_r != 64 && d->d_r != 0))
+    return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+}  // namespace
+
+int mla_cache_write_paged(const mla_dims* d, int32_t T, const void* x, int64_t x_stride,
+                          const float* gamma, float eps, const mla_rope_table* table,
+                          const int32_t* positions, const int64_t* slots, void* cache_pool,
+                          int64_t num_pages, void* stream) {
+  int st = check_write(d, T, x, x_stride, gamma, eps, table, cache_pool, num_pages);
+  if (st) return st;
+  if (T == 0) return MLA_OK;
+  if (!slots || (table && !positions)) return MLA_ERR_INVALID_ARG;
+  if (!aligned_to(slots, 8) || !aligned_to(positions, 4)) return MLA_ERR_ALIGNMENT;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t rows = num_pages * kTileKeys;
+  if (d->dtype == MLA_BF16)
+    return cuda_status(launch_cache_write<__nv_bfloat16>(
+        table, static_cast<const __nv_bfloat16*>(x), x_stride, gamma, eps, positions, slots, T,
+        d->d_c, d->d_r, rows, static_cast<__nv_bfloat16*>(cache_pool), status_ptr(), s));
+  return cuda_status(launch_cache_write<float>(
+      table, static_cast<const float*>(x), x_stride, gamma, eps, positions, slots, T, d->d_c,
+      d->d_r, rows, static_cast<float*>(cache_pool), status_ptr(), s));
+}
+
+int mla_cache_write_fp8_paged(const mla_dims* d, int32_t T, const void* x, int64_t x_stride,
+                              const float* gamma, float eps, const mla_rope_table* table,
+                              const int32_t* query_start, const int32_t* seqlens,
+                              const int32_t* block_table, int32_t max_blocks, void* cache_pool,
+                              float* page_scales, int64_t num_pages, void* stream) {
+  int st = check_write(d, T, x, x_stride, gamma, eps, table, cache_pool, num_pages);
+  if (st) return st;
+  if ((st = check_fp8_paged(d)) || (st = check_pages(d, num_pages, block_table, max_blocks)))
+    return st;
+  if (T == 0) return MLA_OK;
+  if (!query_start || !seqlens || !page_scales) return MLA_ERR_INVALID_ARG;
+  if (!aligned_to(query_start, 4) || !aligned_to(seqlens, 4) || !aligned_to(page_scales, 4))
+    return MLA_ERR_ALIGNMENT;
+  return cuda_status(launch_cache_write_fp8(
+      table, static_cast<const __nv_bfloat16*>(x), x_stride, T, gamma, eps, query_start, seqlens,
+      d->B, d->cache_capacity, d->d_r,
+      PageMap{block_table, max_blocks, num_pages, d->cache_capacity},
+      static_cast<uint8_t*>(cache_pool), page_scales, status_ptr(),
+      static_cast<cudaStream_t>(stream)));
+}
+
+int mla_decode_fp8_paged(const mla_dims* d, const void* q_cat, const void* cache_pool,
+                         const float* page_scales, int64_t num_pages, const int32_t* block_table,
+                         int32_t max_blocks, const int32_t* seqlens, float softmax_scale,
+                         int num_splits, void* workspace, size_t workspace_bytes,
+                         int* splits_used, void* stream) {
+  int st = check_dims(d);
+  if (st) return st;
+  if ((st = check_fp8_paged(d)) || (st = check_pages(d, num_pages, block_table, max_blocks)))
+    return st;
+  if (!q_cat || !cache_pool || !page_scales || !seqlens || num_splits < 0 ||
+      num_splits > kMaxSplits || !(softmax_scale >= 0.f) || softmax_scale == INFINITY)
+    return MLA_ERR_INVALID_ARG;
+  softmax_scale = effective_scale(d, softmax_scale);
+  if (!aligned16(q_cat) || !aligned16(cache_pool) || !aligned16(page_scales) ||
+      !aligned16(seqlens) || (workspace && !aligned16(workspace)))
+    return MLA_ERR_ALIGNMENT;
+  int W = num_splits;
+  if (W == 0) {
+    W = decode_fp8_paged_splits(sm_count(), d->H);
+    const int most = mla_decode_default_splits(d);
+    W = W < most ? W : most;
+    if (W <= 0) return MLA_ERR_CUDA;
+  }
+  const WsLayout l = ws_layout(d, W);
+  if (!workspace || workspace_bytes < l.total) return MLA_ERR_WORKSPACE;
+  if (splits_used) *splits_used = W;
+  float* o_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.o_off);
+  float* lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.lse_off);
+  return cuda_status(launch_decode_fp8_paged(
+      static_cast<const __nv_bfloat16*>(q_cat), static_cast<const uint8_t*>(cache_pool),
+      page_scales, PageMap{block_table, max_blocks, num_pages, d->cache_capacity}, seqlens, d->B,
+      d->H, d->d_r, d->cache_capacity, softmax_scale, W, o_part, lse_part, status_ptr(),
+      g_inject_wait_cycles, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
 // Materialised prefill of one sequence.
 namespace {
 int check_prefill(const mla_dims* d, int32_t T, int64_t L) {
