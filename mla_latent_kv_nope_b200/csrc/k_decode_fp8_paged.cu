@@ -1,132 +1,744 @@
-// Split-KV latent decode over a paged 8-bit cache (simple form: CUDA cores).
+// Split-KV latent decode over a paged 8-bit cache for sm_100a (d_c = 512, d_r =
+// 64 or 0).
 //
 // A page holds 64 rows [512 E4M3 codes || d_r bf16 RoPE keys], all in units of
-// the page's scale.  Per sequence b and head i, over the keys of one work range:
-//   s_j = softmax_scale * scale_page * (q_cat[b,i] . row_j),  online softmax,
+// the page's power-of-two scale.  Per sequence b and head i, over the keys of
+// one work range:
+//   s_j = softmax_scale * scale_page * (q_cat[b,i] . row_j),  softmax over j,
 //   o = sum_j p_j scale_page codes_j
-// One warp per head; a block stages 32 key rows at a time in shared memory.
+//
+// 8-bit products without widening.  The codes go to the tensor cores as they
+// lie in the cache (kind::f8f6f4, twice the 16-bit rate); what is not 8 bits is
+// split into two E4M3 terms, x = hi + lo, each of 4 significant bits:
+//   * a query row times a power of two (largest value in (224, 448]): a bf16
+//     value has 8 significant bits, so hi + lo is exact for values within 2^10
+//     of the largest, and off by at most 2^-18 of it below;
+//   * a probability: hi is rounded to 4 bits, lo the rest, 2^-8 of p together.
+// So both products cost as many tensor cycles as 16-bit ones, but the cache
+// is read, staged and fed at one byte per value and no thread touches it.  The
+// RoPE part is a bf16 product into the same accumulator.
+// The page scale folds into the probability (p_j scale_page enters the second
+// product), so it costs one multiply per key and head group.
+//
+// Range of the probabilities.  E4M3 reaches from 448 to 2^-9, far less than a
+// softmax: with one reference (a running maximum) the keys 2^16 below the
+// largest of the whole sequence would vanish, and thousands of those can carry
+// most of the weight (one early key that outweighs all others).  The reference
+// r therefore follows the tile: it moves when a tile's maximum leaves
+// [r - kFall, r + kRise] (log2), up or down, with O and l rescaled by
+// 2^(r_old - r_new) in fp32; it stays within 2^60 of the largest so far, below
+// which nothing is left to add.  Within a tile of 128 keys values down to
+// 2^-12 of its largest keep a step of at most that largest's 2^-13.
+//
+// Structure: a cluster of two CTAs (128 heads, 64 each) shares every product
+// with cta_group::2, M = 128.  One CTA alone could not: 128 heads x 512 output
+// columns of fp32 fill its tensor memory, and M = 64 products run at half rate.
+// With the pair each CTA holds its 64 heads' O in 256 columns (an M = 128 pair
+// accumulator keeps columns [0, N/2) in lanes 0-63 and [N/2, N) in lanes
+// 64-127).  Per iteration of two pages (128 keys):
+//   S [64 heads each, 128 keys] = Q . K^T: CTA r supplies page r's rows
+//   O [64 heads each, 512] += P . C:     CTA r supplies columns [128 r, +128) and
+//                                        [256 + 128 r, +128) of both pages
+// A CTA thus stages its own page whole (K: codes and RoPE keys, 40 KB, 2
+// stages) and half the columns of both pages again (V: 16 KB per page, 3
+// stages; out of L2), because the operands of a pair product must lie at the
+// same offsets in both CTAs.
+//   warps 0-3  softmax: thread = (head row, page); query split, epilogue
+//   warp 4     K loads (TMA) and page scales;  warp 7  V loads
+//   warp 5     QK^T products (leader); in the other CTA it tells the leader
+//              that its K stage has landed
+//   warp 6     P.C products (leader); the same for V
+// Every wait is bounded (about 2 s of SM cycles); on give-up a CTA raises the
+// abort flag of both, records MLA_ERR_DEVICE_TIMEOUT, drains its own loads and
+// products and exits.
+#include <cuda.h>
 #include <cuda_fp8.h>
 
+#include "common.cuh"
 #include "kernels.h"
+#include "sm100.cuh"
+#include "tensor_map.cuh"
+#include "tile_deal.cuh"
 
 namespace mla {
 
 namespace {
 
-constexpr int kHeads = 8;
-constexpr int kKeys = 32;
-constexpr int kDc = 512;
+using namespace sm100;
 
-__global__ void __launch_bounds__(kHeads * 32)
-decode8_simt_kernel(const __nv_bfloat16* __restrict__ q_cat, const uint8_t* __restrict__ pool,
-                    const float* __restrict__ page_scales, const PageMap pm,
-                    const int32_t* __restrict__ seqlens, int B, int H, int d_r, int64_t cap,
-                    float scale, int W, float* __restrict__ o_part, float* __restrict__ lse_part,
-                    int* __restrict__ status) {
-  extern __shared__ float smem[];
-  const int R = kDc + d_r, ldr = R + 1, row_bytes = kDc + 2 * d_r;
-  float* s_rows = smem;
-  float* s_q = s_rows + kKeys * ldr;
-  const int w = blockIdx.x, h0 = blockIdx.y * kHeads;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = h0 + warp;
-  pdl_wait();
-  int64_t n_units = 0;
-  for (int b = 0; b < B; ++b) n_units += units_of(clamp_len(seqlens[b], cap));
-  if (n_units == 0) return;
-  const int64_t u0 = worker_tile_begin(w, n_units, W), u1 = worker_tile_begin(w + 1, n_units, W);
-  if (u0 >= u1) return;
-  int64_t prefix = 0;
-  for (int b = 0; b < B && prefix < u1; ++b) {
-    const int64_t L = clamp_len(seqlens[b], cap), nt = tiles_of(L), r0 = prefix + kSwitchUnits;
-    const int64_t lo = max(r0, u0), hi = min(r0 + nt, u1);
-    prefix += units_of(L);
-    if (nt == 0 || lo >= hi) continue;
-    const int64_t key_lo = (lo - r0) * kTileKeys, key_hi = min((hi - r0) * int64_t(kTileKeys), L);
-    __syncthreads();
-    for (int i = threadIdx.x; i < kHeads * R; i += blockDim.x) {
-      const int h = h0 + i / R;
-      s_q[i] = h < H ? __bfloat162float(q_cat[(int64_t(b) * H + h) * R + i % R]) : 0.f;
-    }
-    float m = -INFINITY, l = 0.f, acc[kDc / 32];
-#pragma unroll
-    for (int k = 0; k < kDc / 32; ++k) acc[k] = 0.f;
-    for (int64_t k0 = key_lo; k0 < key_hi; k0 += kKeys) {
-      const int nk = int(min(int64_t(kKeys), key_hi - k0));
-      const int64_t row0 = pm.row(b, k0);   // 32 keys never cross a page
-      const float sc = row0 < 0 ? 0.f : page_scales[row0 / kTileKeys];
-      if (row0 < 0 && threadIdx.x == 0) record_status(status, MLA_ERR_BOUNDS);
-      __syncthreads();
-      for (int i = threadIdx.x; i < nk * R; i += blockDim.x) {
-        const int j = i / R, c = i % R;
-        float v = 0.f;
-        if (row0 >= 0) {
-          const uint8_t* row = pool + (row0 + j) * row_bytes;
-          if (c < kDc) {
-            const __half_raw hr = __nv_cvt_fp8_to_halfraw(row[c], __NV_E4M3);
-            v = __half2float(__half(hr)) * sc;
-          } else {
-            v = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row + kDc)[c - kDc]) * sc;
-          }
-        }
-        s_rows[j * ldr + c] = v;
-      }
-      __syncthreads();
-      float s = -INFINITY;
-      if (lane < nk) {
-        const float* q = s_q + warp * R;
-        const float* r = s_rows + lane * ldr;
-        float a = 0.f;
-        for (int c = 0; c < R; ++c) a = fmaf(q[c], r[c], a);
-        s = a * scale;
-      }
-      const float m_new = fmaxf(m, warp_max(s));
-      const float p = lane < nk ? expf(s - m_new) : 0.f;
-      const float alpha = expf(m - m_new);
-      l = l * alpha + warp_sum(p);
-      m = m_new;
-#pragma unroll
-      for (int k = 0; k < kDc / 32; ++k) acc[k] *= alpha;
-      for (int j = 0; j < nk; ++j) {
-        const float pj = __shfl_sync(0xffffffffu, p, j);
-        const float* r = s_rows + j * ldr;
-#pragma unroll
-        for (int k = 0; k < kDc / 32; ++k) acc[k] = fmaf(pj, r[lane + 32 * k], acc[k]);
-      }
-    }
-    if (head < H) {
-      const int slot = b + w;
-      const float inv_l = 1.f / l;
-      float* o = o_part + int64_t(slot) * kDc * H + int64_t(head) * 4;
-#pragma unroll
-      for (int k = 0; k < kDc / 32; ++k) {
-        const int c = lane + 32 * k;
-        o[int64_t(c >> 2) * H * 4 + (c & 3)] = acc[k] * inv_l;
-      }
-      if (lane == 0) lse_part[int64_t(slot) * H + head] = m + logf(l);
+constexpr int kHeadsPerCta = 64;
+constexpr int kDc = 512;
+constexpr int kChunk = 8192;              // 64 rows x 128 bytes, 128-byte swizzle
+constexpr int kKStages = 2, kVStages = 3;
+constexpr int kKBytes = 5 * kChunk;       // 4 chunks of codes, 1 of RoPE keys
+constexpr int kVBytes = 2 * kChunk;
+constexpr int kScaleRing = 4;
+constexpr int kThreads = 256;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 0, kColS = 256;    // O: 2 x 128 columns, S: 2 x 64
+constexpr float kPScale = 6.f;            // probabilities are held times 2^6
+constexpr float kRise = 2.f, kFall = 3.f; // log2: 2^(6 + 2) = 256 <= 448
+constexpr float kTopWindow = 60.f;
+
+constexpr uint32_t kIdescQK = idesc_f16_f32(128, 128, false, false);   // E4M3 is format 0 too
+constexpr uint32_t kIdescRope = idesc_bf16_f32(128, 128, false, false);
+constexpr uint32_t kIdescPV = idesc_f16_f32(128, 256, false, true);
+
+struct Bars {
+  uint64_t kfull[kKStages], peer_k[kKStages];
+  uint64_t vfull[kVStages], peer_v[kVStages], vempty[kVStages];
+  uint64_t s_full[2], s_free[2];
+  uint64_t sc_full[kScaleRing];
+  uint64_t q_ready, p_full, pv_done, o_free, meet;
+  uint64_t qk_drain, pv_drain, never;
+  float scale[kScaleRing][2];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+constexpr size_t kOffQ = 0;                                  // 4 hi, 4 lo, 1 RoPE chunk
+constexpr size_t kOffP = kOffQ + 9 * kChunk;                 // hi, lo
+constexpr size_t kOffK = kOffP + 2 * kChunk;
+constexpr size_t kOffV = kOffK + size_t(kKStages) * kKBytes;
+constexpr size_t kOffBars = kOffV + size_t(kVStages) * kVBytes;
+constexpr size_t kOffMax = kOffBars + (sizeof(Bars) + 15) / 16 * 16;   // [2][2][64] floats
+constexpr size_t kOffRowScale = kOffMax + 2 * 2 * 64 * sizeof(float);  // [64] floats
+constexpr size_t kOffPrefix = kOffRowScale + 64 * sizeof(float);
+constexpr size_t kSmemBytes = kOffPrefix + kTilePrefixSmemBytes + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA");
+
+__device__ __forceinline__ void raise_abort(Bars* bars, int* status) {
+  for (uint32_t r = 0; r < 2; ++r) st_cluster_u32(cluster_map(&bars->abort_flag, r), 1);
+  record_status(status, MLA_ERR_DEVICE_TIMEOUT);
+}
+
+// Warp-uniform bounded wait (all lanes poll; lane 0 owns the limit).  Barriers
+// that the other CTA arrives on are waited for at cluster scope.
+template <bool kCluster>
+__device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                       uint64_t limit = kWaitLimitCycles) {
+  auto poll = [&] {
+    return __all_sync(0xffffffffu, kCluster ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity));
+  };
+  if (poll()) return true;
+  const uint64_t t0 = sm_cycles();
+  for (uint32_t it = 0;; ++it) {
+    if (poll()) return true;
+    if ((it & 63) == 63) {
+      int give_up = 0;
+      if ((threadIdx.x & 31) == 0) give_up = (*abort_flag != 0) || (sm_cycles() - t0 > limit);
+      if (__shfl_sync(0xffffffffu, give_up, 0)) return false;
     }
   }
 }
 
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
+  const __half2 h(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(c), __NV_E4M3));
+  return __half22float2(h);
+}
+
+// Page rows and scales of a run of tiles: lane l holds tile base + l, and the
+// 32 after those are already on their way.
+struct PageWalk {
+  const PageMap& pm;
+  const float* scales;   // or null
+  int b, lane;
+  int64_t base, hi;
+  int64_t row, row_next;
+  float sc, sc_next;
+  __device__ PageWalk(const PageMap& m, const float* s, int b_, int64_t lo, int64_t hi_)
+      : pm(m), scales(s), b(b_), lane(threadIdx.x & 31), base(lo), hi(hi_) {
+    fetch(lo, row, sc);
+    fetch(lo + 32, row_next, sc_next);
+  }
+  __device__ void fetch(int64_t t0, int64_t& r, float& s) const {
+    const int64_t t = t0 + lane;
+    r = t < hi ? pm.tile_row(b, t) : -1;
+    s = scales && r >= 0 ? scales[r / kTileKeys] : 1.f;
+  }
+  // Row (-1: outside the pool) and scale of tile t >= base, the same in all lanes.
+  __device__ void at(int64_t t, int64_t* r, float* s) {
+    if (t >= base + 32) {
+      base += 32;
+      row = row_next, sc = sc_next;
+      fetch(base + 32, row_next, sc_next);
+    }
+    *r = __shfl_sync(0xffffffffu, row, int(t - base));
+    *s = __shfl_sync(0xffffffffu, sc, int(t - base));
+  }
+};
+
+template <int kDr>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
+               const __grid_constant__ CUtensorMap tm_rope,
+               const float* __restrict__ page_scales, const PageMap pm,
+               const __nv_bfloat16* __restrict__ q_cat, const int32_t* __restrict__ seqlens, int B,
+               int H, int64_t cap, float scale_log2, int W, float* __restrict__ o_part,
+               float* __restrict__ lse_part, int* __restrict__ status, uint64_t inject_wait) {
+  constexpr int R = kDc + kDr;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars* bars = reinterpret_cast<Bars*>(smem + kOffBars);
+  const uint32_t rank = cluster_rank();
+  const int g = blockIdx.x, w = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  pdl_wait();
+  TilePrefix tp;
+  const int64_t n_units = build_tile_prefix(smem + kOffPrefix, seqlens, B, cap, &tp);
+  if (n_units == 0) return;      // the same in both CTAs of a pair, as is the range
+  const int64_t u0 = worker_tile_begin(w, n_units, W), u1 = worker_tile_begin(w + 1, n_units, W);
+  if (u0 >= u1) return;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kKStages; ++s) mbar_init(&bars->kfull[s], 1), mbar_init(&bars->peer_k[s], 1);
+    for (int s = 0; s < kVStages; ++s) {
+      mbar_init(&bars->vfull[s], 1);
+      mbar_init(&bars->peer_v[s], 1);
+      mbar_init(&bars->vempty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) mbar_init(&bars->s_full[s], 1), mbar_init(&bars->s_free[s], 8);
+    for (int s = 0; s < kScaleRing; ++s) mbar_init(&bars->sc_full[s], 1);
+    mbar_init(&bars->q_ready, 8);     // the four softmax warps of both CTAs
+    mbar_init(&bars->p_full, 8);
+    mbar_init(&bars->o_free, 8);
+    mbar_init(&bars->pv_done, 1);
+    mbar_init(&bars->meet, 4);
+    mbar_init(&bars->qk_drain, 1);
+    mbar_init(&bars->pv_drain, 1);
+    mbar_init(&bars->never, 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 5) {
+    tmem_alloc_pair(&bars->tmem_base, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  if (threadIdx.x == 128) {
+    tma_prefetch_desc(&tm_codes);
+    if (kDr) tma_prefetch_desc(&tm_rope);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  volatile int* abort_flag = &bars->abort_flag;
+  uint32_t n_issued = 0;     // K or V stages that this producer warp has loaded into
+  bool ok = true;
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ K and scales
+    uint32_t i = 0;
+    for_each_segment(tp, u0, u1, [&](int b, int64_t lo, int64_t hi, int64_t) {
+      PageWalk walk(pm, page_scales, b, lo, hi);
+      for (int64_t t = lo; t < hi; t += 2, ++i) {
+        const int st = i & 1;
+        const bool two = t + 1 < hi;
+        int64_t row[2];
+        float sc[2];
+        walk.at(t, &row[0], &sc[0]);
+        // A pair never straddles the 32 tiles of a walk (both start even).
+        row[1] = -1, sc[1] = 1.f;
+        if (two) walk.at(t + 1, &row[1], &sc[1]);
+        if (i >= 2 && !(ok = wait_w<true>(&bars->s_full[st], ((i >> 1) - 1) & 1, abort_flag)))
+          return false;
+        if (lane == 0) {
+          bars->scale[i & 3][0] = sc[0];
+          bars->scale[i & 3][1] = sc[1];
+          mbar_arrive(&bars->sc_full[i & 3]);
+          if (rank == 0 || two) {
+            int64_t r = rank ? row[1] : row[0];
+            if (r < 0) {   // reads as zeros: past the end of the map
+              record_status(status, MLA_ERR_BOUNDS);
+              r = pm.total_rows(B);
+            }
+            uint8_t* dst = smem + kOffK + st * kKBytes;
+            mbar_arrive_expect_tx(&bars->kfull[st], (kDr ? 5 : 4) * kChunk);
+            for (int c = 0; c < 4; ++c)
+              tma_load_2d(&tm_codes, &bars->kfull[st], dst + c * kChunk, c * 128, int32_t(r));
+            if (kDr) tma_load_2d(&tm_rope, &bars->kfull[st], dst + 4 * kChunk, kDc / 2, int32_t(r));
+          } else {
+            mbar_arrive(&bars->kfull[st]);   // no second page: its scores are masked
+          }
+        }
+        __syncwarp();
+        n_issued = i + 1;
+      }
+      return true;
+    });
+  } else if (warp == 7) {
+    // ------------------------------------------------------------ V
+    uint32_t v = 0;
+    for_each_segment(tp, u0, u1, [&](int b, int64_t lo, int64_t hi, int64_t) {
+      PageWalk walk(pm, nullptr, b, lo, hi);
+      for (int64_t t = lo; t < hi; ++t, ++v) {
+        const int vs = v % kVStages;
+        int64_t r;
+        float unused;
+        walk.at(t, &r, &unused);
+        if (v >= kVStages &&
+            !(ok = wait_w<true>(&bars->vempty[vs], (v / kVStages - 1) & 1, abort_flag)))
+          return false;
+        if (lane == 0) {
+          if (r < 0) r = pm.total_rows(B);
+          uint8_t* dst = smem + kOffV + vs * kVBytes;
+          mbar_arrive_expect_tx(&bars->vfull[vs], kVBytes);
+          for (int h = 0; h < 2; ++h)
+            tma_load_2d(&tm_codes, &bars->vfull[vs], dst + h * kChunk, (2 * h + int(rank)) * 128,
+                        int32_t(r));
+        }
+        __syncwarp();
+        n_issued = v + 1;
+      }
+      return true;
+    });
+  } else if (warp == 5 && rank == 0) {
+    // ------------------------------------------------------------ QK^T (leader)
+    uint32_t i = 0;
+    int seg = 0;
+    const uint64_t qd = smem_desc_sw128(smem_u32(smem + kOffQ), 16, 1024);
+    const uint64_t kd = smem_desc_sw128(smem_u32(smem + kOffK), 16, 1024);
+    // Test hook: a wait on a barrier nothing arrives on, so the give-up path runs.
+    if (inject_wait) ok = wait_w<false>(&bars->never, 0, abort_flag, inject_wait);
+    if (ok) for_each_segment(tp, u0, u1, [&](int, int64_t lo, int64_t hi, int64_t) {
+      if (!(ok = wait_w<true>(&bars->q_ready, seg & 1, abort_flag))) return false;
+      for (int64_t t = lo; t < hi; t += 2, ++i) {
+        const int st = i & 1;
+        const uint32_t ph = (i >> 1) & 1;
+        if (!(ok = wait_w<false>(&bars->kfull[st], ph, abort_flag)) ||
+            !(ok = wait_w<true>(&bars->peer_k[st], ph, abort_flag)) ||
+            (i >= 2 && !(ok = wait_w<true>(&bars->s_free[st], ph ^ 1, abort_flag))))
+          return false;
+        tc_fence_after();
+        const uint32_t d = tmem + kColS + uint32_t(st) * 64u;
+        const uint64_t b0 = kd + uint64_t((uint32_t(st) * kKBytes) >> 4);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int term = 0; term < 2; ++term)
+              mma_f8_ss_pair_w(d, qd + uint64_t(((term * 4 + c) * kChunk + k * 32) >> 4),
+                               b0 + uint64_t((c * kChunk + k * 32) >> 4), kIdescQK,
+                               (c | k | term) != 0);
+        if (kDr) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_bf16_ss_pair_w(d, qd + uint64_t((8 * kChunk + k * 32) >> 4),
+                               b0 + uint64_t((4 * kChunk + k * 32) >> 4), kIdescRope, true);
+        }
+        mma_commit_pair_w(&bars->s_full[st]);
+      }
+      ++seg;
+      return true;
+    });
+    mma_commit_pair_w(&bars->qk_drain);
+    volatile int no_abort = 0;
+    wait_w<true>(&bars->qk_drain, 0, &no_abort);
+  } else if (warp == 6 && rank == 0) {
+    // ------------------------------------------------------------ P.C (leader)
+    uint32_t i = 0, v = 0;
+    int seg = 0;
+    const uint64_t pd = smem_desc_sw128(smem_u32(smem + kOffP), 16, 1024);
+    const uint64_t vd = smem_desc_sw128(smem_u32(smem + kOffV), kChunk, 1024);
+    for_each_segment(tp, u0, u1, [&](int, int64_t lo, int64_t hi, int64_t) {
+      for (int64_t t = lo; t < hi; t += 2, ++i) {
+        if (!(ok = wait_w<true>(&bars->p_full, i & 1, abort_flag))) return false;
+        // The previous sequence's epilogue has read O before it is overwritten.
+        if (t == lo && seg > 0 && !(ok = wait_w<true>(&bars->o_free, (seg - 1) & 1, abort_flag)))
+          return false;
+        for (int p = 0; p < 2 && t + p < hi; ++p, ++v) {
+          const int vs = v % kVStages;
+          const uint32_t ph = (v / kVStages) & 1;
+          if (!(ok = wait_w<false>(&bars->vfull[vs], ph, abort_flag)) ||
+              !(ok = wait_w<true>(&bars->peer_v[vs], ph, abort_flag)))
+            return false;
+          tc_fence_after();
+          const uint64_t a0 = pd + uint64_t((p * 64) >> 4);
+          const uint64_t b0 = vd + uint64_t((uint32_t(vs) * kVBytes) >> 4);
+          const bool fresh = t == lo && p == 0;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int term = 0; term < 2; ++term)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                mma_f8_ss_pair_w(tmem + kColO + uint32_t(h) * 128u,
+                                 a0 + uint64_t((term * kChunk + k * 32) >> 4),
+                                 b0 + uint64_t((h * kChunk + k * 32 * 128) >> 4), kIdescPV,
+                                 !(fresh && k == 0 && term == 0));
+          mma_commit_pair_w(&bars->vempty[vs]);
+        }
+        mma_commit_pair_w(&bars->pv_done);
+      }
+      ++seg;
+      return true;
+    });
+    mma_commit_pair_w(&bars->pv_drain);
+    volatile int no_abort = 0;
+    wait_w<true>(&bars->pv_drain, 0, &no_abort);
+  } else if (warp == 5 || warp == 6) {
+    // ------------------------------------------------- landed loads, to the leader
+    uint32_t n = 0;
+    const bool k_side = warp == 5;
+    for_each_segment(tp, u0, u1, [&](int, int64_t lo, int64_t hi, int64_t) {
+      for (int64_t t = lo; t < hi; t += k_side ? 2 : 1, ++n) {
+        uint64_t* full = k_side ? &bars->kfull[n & 1] : &bars->vfull[n % kVStages];
+        uint64_t* peer = k_side ? &bars->peer_k[n & 1] : &bars->peer_v[n % kVStages];
+        const uint32_t ph = (k_side ? n >> 1 : n / kVStages) & 1;
+        if (!(ok = wait_w<false>(full, ph, abort_flag))) return false;
+        if (lane == 0) mbar_arrive_cluster(cluster_map(peer, 0));
+        __syncwarp();
+      }
+      return true;
+    });
+    // The leader's last arrival on this CTA's barriers.
+    volatile int no_abort = 0;
+    wait_w<true>(k_side ? &bars->qk_drain : &bars->pv_drain, 0, &no_abort);
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int tid = threadIdx.x;             // 0..127
+    const int row = tid & 63, pg = tid >> 6; // head row; page of the pair
+    const int head = g * kHeadsPerCta + row;
+    const uint32_t lanes = tmem + (uint32_t(32 * warp) << 16);
+    float* s_max = reinterpret_cast<float*>(smem + kOffMax);
+    float* s_row = reinterpret_cast<float*>(smem + kOffRowScale);
+    const uint32_t a_q = cluster_map(&bars->q_ready, 0), a_p = cluster_map(&bars->p_full, 0),
+                   a_o = cluster_map(&bars->o_free, 0), a_s0 = cluster_map(&bars->s_free[0], 0),
+                   a_s1 = cluster_map(&bars->s_free[1], 0);
+    uint32_t i = 0, v = 0, n_meet = 0;
+    auto arrive = [&](uint32_t addr) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(addr);
+    };
+    // The four warps meet (bounded, unlike a named barrier).
+    auto meet = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->meet);
+      return ok = wait_w<false>(&bars->meet, n_meet++ & 1, abort_flag);
+    };
+
+    // Splits the query block of sequence b into E4M3 terms: a warp takes 16
+    // rows, 4 at a time (their loads are in flight together).
+    auto write_query = [&](int b) {
+#pragma unroll 1
+      for (int r0 = 16 * warp; r0 < 16 * warp + 16; r0 += 4) {
+        uint4 u[4][3];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int h = g * kHeadsPerCta + r0 + r;
+          const uint4* src = reinterpret_cast<const uint4*>(q_cat + (int64_t(b) * H + h) * R);
+          const uint4 z = make_uint4(0, 0, 0, 0);
+          u[r][0] = h < H ? src[lane] : z;
+          u[r][1] = h < H ? src[lane + 32] : z;
+          u[r][2] = kDr && h < H && lane < kDr / 8 ? src[64 + lane] : z;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int qr = r0 + r;
+          float f[2][8], top = 0.f;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t wd[4] = {u[r][e].x, u[r][e].y, u[r][e].z, u[r][e].w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              f[e][2 * x] = __uint_as_float(wd[x] << 16);
+              f[e][2 * x + 1] = __uint_as_float(wd[x] & 0xFFFF0000u);
+              top = fmaxf(top, fmaxf(fabsf(f[e][2 * x]), fabsf(f[e][2 * x + 1])));
+            }
+          }
+          top = warp_max(top);
+          // Smallest k with top <= 448 * 2^k; kept where 2^k and 2^-k are normal.
+          int k = 0;
+          if (top > 0.f) {
+            const float m = frexpf(top, &k);
+            k = min(max(m <= 0.875f ? k - 9 : k - 8, -120), 120);
+          }
+          const float inv = ldexpf(1.f, -k);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float a = f[e][2 * x] * inv, c = f[e][2 * x + 1] * inv;
+              hi[x] = e4m3x2(a, c);
+              const float2 back = from_e4m3x2(hi[x]);
+              lo[x] = e4m3x2(a - back.x, c - back.y);
+            }
+            const int un = lane + 32 * e;    // 8 codes: half of 16-byte unit (un % 16) / 2
+            const int off = (un / 16) * kChunk + qr * 128 + ((((un % 16) >> 1) ^ (qr & 7)) * 16) +
+                            (un & 1) * 8;
+            *reinterpret_cast<uint2*>(smem + kOffQ + off) =
+                make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+            *reinterpret_cast<uint2*>(smem + kOffQ + 4 * kChunk + off) =
+                make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+          }
+          if (kDr && lane < kDr / 8) {
+            const uint32_t wd[4] = {u[r][2].x, u[r][2].y, u[r][2].z, u[r][2].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const __nv_bfloat162 p = __floats2bfloat162_rn(
+                  __uint_as_float(wd[x] << 16) * inv, __uint_as_float(wd[x] & 0xFFFF0000u) * inv);
+              o[x] = *reinterpret_cast<const uint32_t*>(&p);
+            }
+            *reinterpret_cast<uint4*>(smem + kOffQ + 8 * kChunk + qr * 128 +
+                                      ((lane ^ (qr & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          if (lane == 0) s_row[qr] = ldexpf(1.f, k);
+        }
+      }
+      fence_proxy_async_smem();
+      arrive(a_q);
+    };
+
+    const int first_b = tp.next_sequence(-1, u0, u1);
+    if (first_b >= 0) write_query(first_b);
+    for_each_segment(tp, u0, u1, [&](int b, int64_t lo, int64_t hi, int64_t L) {
+      if (!meet()) return false;                       // every row's factor is written
+      const float row_scale = s_row[row] * scale_log2;
+      float ref = 0.f, top = -INFINITY, l_sum = 0.f;   // ref: set by the first tile
+      for (int64_t t = lo; t < hi; t += 2, ++i) {
+        const int sb = i & 1;
+        if (!(ok = wait_w<true>(&bars->s_full[sb], (i >> 1) & 1, abort_flag))) return false;
+        tc_fence_after();
+        uint32_t x0[32], x1[32];
+        tmem_ld32(lanes + kColS + uint32_t(sb) * 64u, x0);
+        tmem_ld32(lanes + kColS + uint32_t(sb) * 64u + 32u, x1);
+        if (!(ok = wait_w<false>(&bars->sc_full[i & 3], (i >> 2) & 1, abort_flag))) return false;
+        const float sc = bars->scale[i & 3][pg];
+        tmem_wait_ld();
+        tc_fence_before();
+        arrive(sb ? a_s1 : a_s0);
+
+        const int64_t left = t + pg < hi ? L - (t + pg) * kTileKeys : 0;
+        const int valid = int(min(left, int64_t(kTileKeys)));
+        if (valid < kTileKeys) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (j >= valid) x0[j] = 0xFF800000u;        // -inf
+            if (j + 32 >= valid) x1[j] = 0xFF800000u;
+          }
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          mx = fmaxf(mx, fmaxf(__uint_as_float(x0[j]), __uint_as_float(x1[j])));
+        const float f = row_scale * sc, lsc = log2f(sc);
+        float mt = mx * f + lsc;                        // log2 of the largest p * scale
+        s_max[(sb * 2 + pg) * 64 + row] = mt;
+        if (!meet()) return false;
+        mt = fmaxf(mt, s_max[(sb * 2 + (pg ^ 1)) * 64 + row]);
+
+        float alpha = 1.f;
+        if (t == lo) {
+          ref = top = mt;
+        } else {
+          top = fmaxf(top, mt);
+          const float to = fmaxf(mt, top - kTopWindow);
+          if (to > ref + kRise || to < ref - kFall) {
+            alpha = ex2_approx(ref - to);
+            ref = to;
+            l_sum *= alpha;
+          }
+        }
+        const float shift = lsc + kPScale - ref;
+        float sum = 0.f;
+        uint32_t hi8[16], lo8[16];
+        auto split4 = [&](const uint32_t* s, uint32_t* h, uint32_t* l) {
+          float p[4], q[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[e] = ex2_approx(fmaf(__uint_as_float(s[e]), f, shift));
+            sum += p[e];
+            q[e] = __uint_as_float((__float_as_uint(p[e]) + 0x00080000u) & 0xFFF00000u);
+          }
+          *h = e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16);
+          *l = e4m3x2(p[0] - q[0], p[1] - q[1]) | (e4m3x2(p[2] - q[2], p[3] - q[3]) << 16);
+        };
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          split4(x0 + 4 * j, hi8 + j, lo8 + j);
+          split4(x1 + 4 * j, hi8 + 8 + j, lo8 + 8 + j);
+        }
+        l_sum = fmaf(sum, 1.f / sc, l_sum);
+
+        // P(i - 1) has been read and O holds its product.
+        if (i > 0 && !(ok = wait_w<true>(&bars->pv_done, (i - 1) & 1, abort_flag))) return false;
+        tc_fence_after();
+        if (t != lo && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < 256; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(lanes + kColO + uint32_t(c), r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+            tmem_st32(lanes + kColO + uint32_t(c), r);
+          }
+          tmem_wait_st();
+        }
+        uint8_t* prow = smem + kOffP + row * 128;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int at = ((pg * 4 + u) ^ (row & 7)) * 16;
+          *reinterpret_cast<uint4*>(prow + at) =
+              make_uint4(hi8[4 * u], hi8[4 * u + 1], hi8[4 * u + 2], hi8[4 * u + 3]);
+          *reinterpret_cast<uint4*>(prow + kChunk + at) =
+              make_uint4(lo8[4 * u], lo8[4 * u + 1], lo8[4 * u + 2], lo8[4 * u + 3]);
+        }
+        // Rows past the sequence's end may hold anything, NaN codes among it:
+        // their weight is 0, so they are zeroed in the staged page.
+#pragma unroll 1
+        for (int p = 0; p < 2 && t + p < hi; ++p, ++v) {
+          const int64_t rows = L - (t + p) * kTileKeys;
+          if (rows >= kTileKeys) continue;
+          const int vs = v % kVStages;
+          if (!(ok = wait_w<false>(&bars->vfull[vs], (v / kVStages) & 1, abort_flag))) return false;
+          uint8_t* stage = smem + kOffV + vs * kVBytes;
+          for (int u = tid; u < (kTileKeys - int(rows)) * 16; u += 128)
+            *reinterpret_cast<uint4*>(stage + (u & 1) * kChunk + (int(rows) + u / 16) * 128 +
+                                      ((u / 2) % 8) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        arrive(a_p);
+      }
+      // Every QK^T of this sequence has been read back: load the next query.
+      const int nb = tp.next_sequence(b, u0, u1);
+      if (nb >= 0) write_query(nb);
+      // Epilogue: normalised partial output and log-sum-exp.
+      // The two halves' sums meet in the buffer that the last tile did not use
+      // (some warp may still be reading the other; the next sequence's first
+      // meeting frees this one).
+      float* s_sum = s_max + (i & 1) * 2 * 64;
+      s_sum[pg * 64 + row] = l_sum;
+      if (!meet()) return false;
+      const float l_row = l_sum + s_sum[(pg ^ 1) * 64 + row];
+      if (!(ok = wait_w<true>(&bars->pv_done, (i - 1) & 1, abort_flag))) return false;
+      tc_fence_after();
+      const float inv = 1.f / l_row;
+      const int slot = b + w;
+      // Partials are o_part[slot][d_c / 4][H][4]: a warp stores 32 consecutive
+      // heads of one 4-column group (512 contiguous bytes), kept in L2 for the
+      // combine that reads them next.
+      const uint64_t keep = l2_policy_evict_last();
+#pragma unroll 1
+      for (int c = 0; c < 256; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(lanes + kColO + uint32_t(c), r);
+        tmem_wait_ld();
+        // Accumulator column c of half h = c / 128 is latent column
+        // 256 h + 128 pg + c % 128.
+        const int col = (c / 128) * 256 + pg * 128 + c % 128;
+        float* dst = o_part + ((int64_t(slot) * (kDc / 4) + col / 4) * H + head) * 4;
+        if (head < H) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            st_global_f4_hint(dst + int64_t(e) * H * 4,
+                              make_float4(__uint_as_float(r[4 * e]) * inv,
+                                          __uint_as_float(r[4 * e + 1]) * inv,
+                                          __uint_as_float(r[4 * e + 2]) * inv,
+                                          __uint_as_float(r[4 * e + 3]) * inv),
+                              keep);
+        }
+      }
+      if (pg == 0 && head < H)
+        lse_part[int64_t(slot) * H + head] = (log2f(l_row) + ref - kPScale) * 0.69314718055994531f;
+      tc_fence_before();
+      arrive(a_o);
+      return true;
+    });
+  }
+  if (!ok && lane == 0) raise_abort(bars, status);
+
+  // Every role has stopped.  The loads that this CTA issued land before its
+  // shared memory is released (after a give-up some were never waited for), and
+  // neither CTA leaves while the other's products may still read from it.
+  __syncwarp();
+  if (lane == 0 && (warp == 4 || warp == 7)) {
+    volatile int no_abort = 0;
+    const uint32_t n_st = warp == 4 ? kKStages : kVStages;
+    for (uint32_t k = (n_issued > n_st ? n_issued - n_st : 0); k < n_issued; ++k)
+      mbar_wait(warp == 4 ? &bars->kfull[k % n_st] : &bars->vfull[k % n_st], (k / n_st) & 1,
+                &no_abort, kWaitLimitCycles);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// Byte map over the rows of the pool: boxes of 128 codes x 64 rows, 128-byte
+// swizzled; rows past the end read as zeros.
+bool make_code_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes) {
+  EncodeTiledFnT fn = encode_tiled_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {row_bytes, rows};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {128, cuuint32_t(kTileKeys)};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kDr, typename... Args>
+cudaError_t launch_t(dim3 grid, cudaStream_t stream, Args... args) {
+  static bool attr_done[64] = {false};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_done[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(decode8_kernel<kDr>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         int(kSmemBytes));
+    if (e != cudaSuccess) return e;
+    attr_done[dev] = true;
+  }
+  return launch_pdl(decode8_kernel<kDr>, grid, dim3(kThreads), kSmemBytes, stream, args...);
+}
+
+inline int head_pairs(int H) { return (H + 2 * kHeadsPerCta - 1) / (2 * kHeadsPerCta); }
+
 }  // namespace
 
 int decode_fp8_paged_splits(int sms, int H) {
-  const int groups = (H + kHeads - 1) / kHeads;
-  return (2 * sms + groups - 1) / groups;
+  const int W = sms / (2 * head_pairs(H));
+  return W < 1 ? 1 : W;
 }
 
 cudaError_t launch_decode_fp8_paged(const __nv_bfloat16* q_cat, const uint8_t* pool,
                                     const float* page_scales, const PageMap& pm,
                                     const int32_t* seqlens, int B, int H, int d_r, int64_t cap,
                                     float scale, int W, float* o_part, float* lse_part,
-                                    int* status, uint64_t, cudaStream_t stream) {
-  const int R = kDc + d_r;
-  const size_t smem = sizeof(float) * (size_t(kKeys) * (R + 1) + size_t(kHeads) * R);
-  cudaError_t e = cudaFuncSetAttribute(decode8_simt_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(decode8_simt_kernel, dim3(W, (H + kHeads - 1) / kHeads), dim3(kHeads * 32),
-                    smem, stream, q_cat, pool, page_scales, pm, seqlens, B, H, d_r, cap, scale, W,
-                    o_part, lse_part, status);
+                                    int* status, uint64_t inject_wait, cudaStream_t stream) {
+  const uint64_t rows = uint64_t(pm.total_rows(B)), row_bytes = kDc + 2 * d_r;
+  CUtensorMap tm_codes, tm_rope;
+  if (!make_code_map(&tm_codes, pool, rows, row_bytes)) return cudaErrorInvalidValue;
+  tm_rope = tm_codes;
+  // The same rows viewed as bf16: the RoPE keys are columns 256 .. 319.
+  if (d_r && !make_map16(&tm_rope, pool, rows, row_bytes / 2, row_bytes / 2, kTileKeys))
+    return cudaErrorInvalidValue;
+  const dim3 grid(2 * head_pairs(H), W);
+  const float scale_log2 = scale * 1.4426950408889634f;
+  auto launch = d_r ? launch_t<64, CUtensorMap, CUtensorMap, const float*, PageMap,
+                               const __nv_bfloat16*, const int32_t*, int, int, int64_t, float, int,
+                               float*, float*, int*, uint64_t>
+                    : launch_t<0, CUtensorMap, CUtensorMap, const float*, PageMap,
+                               const __nv_bfloat16*, const int32_t*, int, int, int64_t, float, int,
+                               float*, float*, int*, uint64_t>;
+  return launch(grid, stream, tm_codes, tm_rope, page_scales, pm, q_cat, seqlens, B, H, cap,
+                scale_log2, W, o_part, lse_part, status, inject_wait);
 }
 
 }  // namespace mla
