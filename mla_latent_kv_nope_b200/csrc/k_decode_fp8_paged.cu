@@ -43,11 +43,15 @@
 // stages) and half the columns of both pages again (V: 16 KB per page, 3
 // stages; out of L2), because the operands of a pair product must lie at the
 // same offsets in both CTAs.
-//   warps 0-3  softmax: thread = (head row, page); query split, epilogue
-//   warp 4     K loads (TMA) and page scales;  warp 7  V loads
-//   warp 5     QK^T products (leader); in the other CTA it tells the leader
-//              that its K stage has landed
-//   warp 6     P.C products (leader); the same for V
+//   warps 0-7  softmax: thread = (head row, page, half of the page's keys);
+//              query split, epilogue
+//   warp 8     K loads (TMA) and page scales;  warp 10  V loads
+//   warp 9     QK^T products (leader); in the other CTA it tells the leader that
+//              a K stage has landed
+//   warp 11    P.C products (leader); the same for V
+// The softmax loop is kept short: with 64 keys a thread, unrolled, its code
+// overran the instruction cache and a tile took 5300 cycles, most of them
+// waiting for instructions.
 // Every wait is bounded (about 2 s of SM cycles); on give-up a CTA raises the
 // abort flag of both, records MLA_ERR_DEVICE_TIMEOUT, drains its own loads and
 // products and exits.
@@ -58,7 +62,6 @@
 #include "kernels.h"
 #include "sm100.cuh"
 #include "tensor_map.cuh"
-#include "tile_deal.cuh"
 
 namespace mla {
 
@@ -69,42 +72,46 @@ using namespace sm100;
 constexpr int kHeadsPerCta = 64;
 constexpr int kDc = 512;
 constexpr int kChunk = 8192;              // 64 rows x 128 bytes, 128-byte swizzle
-constexpr int kKStages = 2, kVStages = 3;
+constexpr int kKStages = 2, kVStages = 3;   // V: and P, page by page
 constexpr int kKBytes = 5 * kChunk;       // 4 chunks of codes, 1 of RoPE keys
 constexpr int kVBytes = 2 * kChunk;
-constexpr int kScaleRing = 4;
-constexpr int kThreads = 256;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
+constexpr int kKWarp = kSoftmaxWarps, kQkWarp = kKWarp + 1, kVWarp = kKWarp + 2,
+              kPvWarp = kKWarp + 3;
+constexpr int kThreads = kSoftmaxThreads + 4 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256;    // O: 2 x 128 columns, S: 2 x 64
-constexpr float kPScale = 6.f;            // probabilities are held times 2^6
-constexpr float kRise = 2.f, kFall = 3.f; // log2: 2^(6 + 2) = 256 <= 448
+constexpr float kPScale = 6.75f;          // probabilities are held times 2^6.75
+constexpr float kRise = 2.f, kFall = 13.f;   // log2; 2^(6.75 + 2) = 430.5 <= 448
+// Where a reference starts above the maximum of the tile that moves it: the
+// first one, a higher one (the next are likely lower) and a lower one.
+constexpr float kLeadFirst = 8.f, kLeadUp = 6.f, kLeadDown = 9.f;
 constexpr float kTopWindow = 60.f;
 
 constexpr uint32_t kIdescQK = idesc_f16_f32(128, 128, false, false);   // E4M3 is format 0 too
 constexpr uint32_t kIdescRope = idesc_bf16_f32(128, 128, false, false);
 constexpr uint32_t kIdescPV = idesc_f16_f32(128, 256, false, true);
+constexpr uint32_t kE5m2A = 1u << 7;      // A's format field: E5M2 (lo) instead of E4M3 (hi)
 
 struct Bars {
-  uint64_t kfull[kKStages], peer_k[kKStages];
-  uint64_t vfull[kVStages], peer_v[kVStages], vempty[kVStages];
+  uint64_t kfull[kKStages];   // leader's: both CTAs' stages have landed
+  uint64_t vfull[kVStages], vempty[kVStages];
   uint64_t s_full[2], s_free[2];
-  uint64_t sc_full[kScaleRing];
-  uint64_t q_ready, p_full, pv_done, o_free, meet;
-  uint64_t qk_drain, pv_drain, never;
-  float scale[kScaleRing][2];
+  uint64_t p_full[2], pv_done[2];
+  uint64_t q_ready, o_free, qk_drain, pv_drain, never;
   uint32_t tmem_base;
   int abort_flag;
 };
 
 constexpr size_t kOffQ = 0;                                  // 4 hi, 4 lo, 1 RoPE chunk
-constexpr size_t kOffP = kOffQ + 9 * kChunk;                 // hi, lo
-constexpr size_t kOffK = kOffP + 2 * kChunk;
+constexpr size_t kOffP = kOffQ + 9 * kChunk;                 // rows of [64 hi, 64 lo]
+constexpr size_t kOffK = kOffP + size_t(kVStages) * kChunk;
 constexpr size_t kOffV = kOffK + size_t(kKStages) * kKBytes;
 constexpr size_t kOffBars = kOffV + size_t(kVStages) * kVBytes;
-constexpr size_t kOffMax = kOffBars + (sizeof(Bars) + 15) / 16 * 16;   // [2][2][64] floats
-constexpr size_t kOffRowScale = kOffMax + 2 * 2 * 64 * sizeof(float);  // [64] floats
-constexpr size_t kOffPrefix = kOffRowScale + 64 * sizeof(float);
-constexpr size_t kSmemBytes = kOffPrefix + kTilePrefixSmemBytes + 1024;
+constexpr size_t kOffMax = kOffBars + (sizeof(Bars) + 15) / 16 * 16;   // [2][4][64] floats
+constexpr size_t kOffRowScale = kOffMax + 2 * 4 * 64 * sizeof(float);  // [64] floats
+constexpr size_t kSmemBytes = kOffRowScale + 64 * sizeof(float);
 static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA");
 
 __device__ __forceinline__ void raise_abort(Bars* bars, int* status) {
@@ -112,19 +119,14 @@ __device__ __forceinline__ void raise_abort(Bars* bars, int* status) {
   record_status(status, MLA_ERR_DEVICE_TIMEOUT);
 }
 
-// Warp-uniform bounded wait (all lanes poll; lane 0 owns the limit).  Barriers
-// that the other CTA arrives on are waited for at cluster scope.
-template <bool kCluster>
+// Warp-uniform bounded wait (all lanes poll; lane 0 owns the limit).
 __device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                        uint64_t limit = kWaitLimitCycles) {
-  auto poll = [&] {
-    return __all_sync(0xffffffffu, kCluster ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity));
-  };
-  if (poll()) return true;
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
   const uint64_t t0 = sm_cycles();
-  for (uint32_t it = 0;; ++it) {
-    if (poll()) return true;
-    if ((it & 63) == 63) {
+  for (;;) {
+    if (__all_sync(0xffffffffu, mbar_try_for(bar, parity, 20000))) return true;
+    {
       int give_up = 0;
       if ((threadIdx.x & 31) == 0) give_up = (*abort_flag != 0) || (sm_cycles() - t0 > limit);
       if (__shfl_sync(0xffffffffu, give_up, 0)) return false;
@@ -138,6 +140,96 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
 __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
   const __half2 h(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(c), __NV_E4M3));
   return __half22float2(h);
+}
+
+// The sequences whose tiles lie in this worker's range of work units (as in
+// tile_deal.cuh, for any batch size): every role walks them by itself from the
+// first one, whose number and unit prefix the block finds together.
+struct Segments {
+  const int32_t* seqlens;
+  int B, b;             // b: the sequence after the current one
+  int64_t cap, pre, u0, u1;
+  int cur;              // the current sequence, its tiles [lo, hi) and length
+  int64_t lo, hi, L;
+  __device__ bool next() {
+    while (b < B && pre < u1) {
+      cur = b++;
+      L = clamp_len(seqlens[cur], cap);
+      const int64_t nt = tiles_of(L), r0 = pre + kSwitchUnits;
+      if (nt == 0) continue;
+      pre = r0 + nt;
+      lo = max(r0, u0) - r0;
+      hi = min(r0 + nt, u1) - r0;
+      if (lo < hi) return true;
+    }
+    return false;
+  }
+};
+
+// All threads; `scratch` is shared memory for kThreads / 32 + 2 values.  False
+// if the worker has no units.
+__device__ __forceinline__ bool find_segments(const int32_t* seqlens, int B, int64_t cap, int w,
+                                              int W, int64_t* scratch, Segments* out) {
+  constexpr int kWarps = kThreads / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t sum = 0;
+  for (int b = threadIdx.x; b < B; b += kThreads) sum += units_of(clamp_len(seqlens[b], cap));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) scratch[warp] = sum;
+  __syncthreads();
+  int64_t total = 0;
+  for (int k = 0; k < kWarps; ++k) total += scratch[k];
+  __syncthreads();
+  const int64_t u0 = worker_tile_begin(w, total, W), u1 = worker_tile_begin(w + 1, total, W);
+  if (u0 >= u1) return false;
+  // The sequence that unit u0 belongs to, kThreads of them at a time.
+  int64_t base = 0;
+  for (int b0 = 0;; b0 += kThreads) {
+    const int b = b0 + int(threadIdx.x);
+    const int64_t n = b < B ? units_of(clamp_len(seqlens[b], cap)) : 0;
+    int64_t e = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, e, o);
+      if (lane >= o) e += u;
+    }
+    if (lane == 31) scratch[warp] = e;
+    __syncthreads();
+    int64_t chunk = 0;
+    for (int k = 0; k < kWarps; ++k) {
+      if (k < warp) e += scratch[k];
+      chunk += scratch[k];
+    }
+    e += base;
+    if (u0 < e && u0 >= e - n) scratch[kWarps] = b, scratch[kWarps + 1] = e - n;
+    __syncthreads();
+    base += chunk;
+    if (u0 < base) break;      // u0 < total, so some chunk holds it
+  }
+  *out = Segments{seqlens, B, int(scratch[kWarps]), cap, scratch[kWarps + 1], u0, u1, 0, 0, 0, 0};
+  __syncthreads();             // before the scratch is used for anything else
+  return true;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 // Page rows and scales of a run of tiles: lane l holds tile base + l, and the
@@ -180,35 +272,32 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
                int H, int64_t cap, float scale_log2, int W, float* __restrict__ o_part,
                float* __restrict__ lse_part, int* __restrict__ status, uint64_t inject_wait) {
   constexpr int R = kDc + kDr;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // The swizzled operands need 1024-byte alignment; the kernel has no other
+  // shared memory, so the array starts on it.
+  extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bars = reinterpret_cast<Bars*>(smem + kOffBars);
   const uint32_t rank = cluster_rank();
   const int g = blockIdx.x, w = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   pdl_wait();
-  TilePrefix tp;
-  const int64_t n_units = build_tile_prefix(smem + kOffPrefix, seqlens, B, cap, &tp);
-  if (n_units == 0) return;      // the same in both CTAs of a pair, as is the range
-  const int64_t u0 = worker_tile_begin(w, n_units, W), u1 = worker_tile_begin(w + 1, n_units, W);
-  if (u0 >= u1) return;
+  Segments seg;
+  // False: the same in both CTAs of a pair.
+  if (!find_segments(seqlens, B, cap, w, W, reinterpret_cast<int64_t*>(smem), &seg)) return;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kKStages; ++s) mbar_init(&bars->kfull[s], 1), mbar_init(&bars->peer_k[s], 1);
+    // The leader's also wait for the other CTA's word that its stage has landed.
+    const uint32_t n_full = rank == 0 ? 2 : 1;
+    for (int s = 0; s < kKStages; ++s) mbar_init(&bars->kfull[s], n_full);
     for (int s = 0; s < kVStages; ++s) {
-      mbar_init(&bars->vfull[s], 1);
-      mbar_init(&bars->peer_v[s], 1);
+      mbar_init(&bars->vfull[s], n_full);
       mbar_init(&bars->vempty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) mbar_init(&bars->s_full[s], 1), mbar_init(&bars->s_free[s], 8);
-    for (int s = 0; s < kScaleRing; ++s) mbar_init(&bars->sc_full[s], 1);
-    mbar_init(&bars->q_ready, 8);     // the four softmax warps of both CTAs
-    mbar_init(&bars->p_full, 8);
-    mbar_init(&bars->o_free, 8);
-    mbar_init(&bars->pv_done, 1);
-    mbar_init(&bars->meet, 4);
+    for (int s = 0; s < 2; ++s) mbar_init(&bars->s_full[s], 1), mbar_init(&bars->s_free[s], 2 * kSoftmaxWarps);
+    mbar_init(&bars->q_ready, 2 * kSoftmaxWarps);   // the softmax warps of both CTAs
+    mbar_init(&bars->o_free, 2 * kSoftmaxWarps);
+    for (int s = 0; s < 2; ++s)
+      mbar_init(&bars->p_full[s], 2 * kSoftmaxWarps), mbar_init(&bars->pv_done[s], 1);
     mbar_init(&bars->qk_drain, 1);
     mbar_init(&bars->pv_drain, 1);
     mbar_init(&bars->never, 1);
@@ -216,11 +305,11 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (warp == 5) {
+  if (warp == kQkWarp) {
     tmem_alloc_pair(&bars->tmem_base, kTmemCols);
     tmem_relinquish_pair();
   }
-  if (threadIdx.x == 128) {
+  if (threadIdx.x == 32 * kKWarp) {
     tma_prefetch_desc(&tm_codes);
     if (kDr) tma_prefetch_desc(&tm_rope);
   }
@@ -233,28 +322,21 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
   uint32_t n_issued = 0;     // K or V stages that this producer warp has loaded into
   bool ok = true;
 
-  if (warp == 4) {
+  if (warp == kKWarp) {
     // ------------------------------------------------------------ K and scales
     uint32_t i = 0;
-    for_each_segment(tp, u0, u1, [&](int b, int64_t lo, int64_t hi, int64_t) {
-      PageWalk walk(pm, page_scales, b, lo, hi);
+    while (ok && seg.next()) {
+      const int64_t lo = seg.lo, hi = seg.hi;
+      PageWalk walk(pm, nullptr, seg.cur, lo, hi);
       for (int64_t t = lo; t < hi; t += 2, ++i) {
         const int st = i & 1;
         const bool two = t + 1 < hi;
-        int64_t row[2];
-        float sc[2];
-        walk.at(t, &row[0], &sc[0]);
-        // A pair never straddles the 32 tiles of a walk (both start even).
-        row[1] = -1, sc[1] = 1.f;
-        if (two) walk.at(t + 1, &row[1], &sc[1]);
-        if (i >= 2 && !(ok = wait_w<true>(&bars->s_full[st], ((i >> 1) - 1) & 1, abort_flag)))
-          return false;
+        int64_t r = -1;
+        float unused;
+        if (rank == 0 || two) walk.at(t + rank, &r, &unused);
+        if (i >= 2 && !(ok = wait_w(&bars->s_full[st], ((i >> 1) - 1) & 1, abort_flag))) break;
         if (lane == 0) {
-          bars->scale[i & 3][0] = sc[0];
-          bars->scale[i & 3][1] = sc[1];
-          mbar_arrive(&bars->sc_full[i & 3]);
           if (rank == 0 || two) {
-            int64_t r = rank ? row[1] : row[0];
             if (r < 0) {   // reads as zeros: past the end of the map
               record_status(status, MLA_ERR_BOUNDS);
               r = pm.total_rows(B);
@@ -271,21 +353,20 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
         __syncwarp();
         n_issued = i + 1;
       }
-      return true;
-    });
-  } else if (warp == 7) {
+    }
+  } else if (warp == kVWarp) {
     // ------------------------------------------------------------ V
     uint32_t v = 0;
-    for_each_segment(tp, u0, u1, [&](int b, int64_t lo, int64_t hi, int64_t) {
-      PageWalk walk(pm, nullptr, b, lo, hi);
-      for (int64_t t = lo; t < hi; ++t, ++v) {
+    while (ok && seg.next()) {
+      PageWalk walk(pm, nullptr, seg.cur, seg.lo, seg.hi);
+      for (int64_t t = seg.lo; t < seg.hi; ++t, ++v) {
         const int vs = v % kVStages;
         int64_t r;
         float unused;
         walk.at(t, &r, &unused);
         if (v >= kVStages &&
-            !(ok = wait_w<true>(&bars->vempty[vs], (v / kVStages - 1) & 1, abort_flag)))
-          return false;
+            !(ok = wait_w(&bars->vempty[vs], (v / kVStages - 1) & 1, abort_flag)))
+          break;
         if (lane == 0) {
           if (r < 0) r = pm.total_rows(B);
           uint8_t* dst = smem + kOffV + vs * kVBytes;
@@ -297,29 +378,26 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
         __syncwarp();
         n_issued = v + 1;
       }
-      return true;
-    });
-  } else if (warp == 5 && rank == 0) {
+    }
+  } else if (warp == kQkWarp && rank == 0) {
     // ------------------------------------------------------------ QK^T (leader)
-    uint32_t i = 0;
-    int seg = 0;
+    uint32_t i = 0, n_seg = 0;
     const uint64_t qd = smem_desc_sw128(smem_u32(smem + kOffQ), 16, 1024);
     const uint64_t kd = smem_desc_sw128(smem_u32(smem + kOffK), 16, 1024);
     // Test hook: a wait on a barrier nothing arrives on, so the give-up path runs.
-    if (inject_wait) ok = wait_w<false>(&bars->never, 0, abort_flag, inject_wait);
-    if (ok) for_each_segment(tp, u0, u1, [&](int, int64_t lo, int64_t hi, int64_t) {
-      if (!(ok = wait_w<true>(&bars->q_ready, seg & 1, abort_flag))) return false;
-      for (int64_t t = lo; t < hi; t += 2, ++i) {
+    if (inject_wait) ok = wait_w(&bars->never, 0, abort_flag, inject_wait);
+    for (; ok && seg.next(); ++n_seg) {
+      if (!(ok = wait_w(&bars->q_ready, n_seg & 1, abort_flag))) break;
+      for (int64_t t = seg.lo; t < seg.hi; t += 2, ++i) {
         const int st = i & 1;
         const uint32_t ph = (i >> 1) & 1;
-        if (!(ok = wait_w<false>(&bars->kfull[st], ph, abort_flag)) ||
-            !(ok = wait_w<true>(&bars->peer_k[st], ph, abort_flag)) ||
-            (i >= 2 && !(ok = wait_w<true>(&bars->s_free[st], ph ^ 1, abort_flag))))
-          return false;
+        if (!(ok = wait_w(&bars->kfull[st], ph, abort_flag)) ||
+            (i >= 2 && !(ok = wait_w(&bars->s_free[st], ph ^ 1, abort_flag))))
+          break;
         tc_fence_after();
         const uint32_t d = tmem + kColS + uint32_t(st) * 64u;
         const uint64_t b0 = kd + uint64_t((uint32_t(st) * kKBytes) >> 4);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -336,34 +414,31 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
         }
         mma_commit_pair_w(&bars->s_full[st]);
       }
-      ++seg;
-      return true;
-    });
+    }
     mma_commit_pair_w(&bars->qk_drain);
     volatile int no_abort = 0;
-    wait_w<true>(&bars->qk_drain, 0, &no_abort);
-  } else if (warp == 6 && rank == 0) {
+    wait_w(&bars->qk_drain, 0, &no_abort);
+  } else if (warp == kPvWarp && rank == 0) {
     // ------------------------------------------------------------ P.C (leader)
-    uint32_t i = 0, v = 0;
-    int seg = 0;
+    // A second issuing warp: a product's issue blocks while the tensor pipe is
+    // busy, and the waits before one product are hidden behind the other's.
+    uint32_t i = 0, v = 0, n_seg = 0;
     const uint64_t pd = smem_desc_sw128(smem_u32(smem + kOffP), 16, 1024);
     const uint64_t vd = smem_desc_sw128(smem_u32(smem + kOffV), kChunk, 1024);
-    for_each_segment(tp, u0, u1, [&](int, int64_t lo, int64_t hi, int64_t) {
-      for (int64_t t = lo; t < hi; t += 2, ++i) {
-        if (!(ok = wait_w<true>(&bars->p_full, i & 1, abort_flag))) return false;
+    for (; ok && seg.next(); ++n_seg) {
+      for (int64_t t = seg.lo; t < seg.hi; t += 2, ++i) {
         // The previous sequence's epilogue has read O before it is overwritten.
-        if (t == lo && seg > 0 && !(ok = wait_w<true>(&bars->o_free, (seg - 1) & 1, abort_flag)))
-          return false;
-        for (int p = 0; p < 2 && t + p < hi; ++p, ++v) {
+        if (t == seg.lo && n_seg > 0 && !(ok = wait_w(&bars->o_free, (n_seg - 1) & 1, abort_flag)))
+          break;
+        if (!(ok = wait_w(&bars->p_full[i & 1], (i >> 1) & 1, abort_flag))) break;
+#pragma unroll 1
+        for (int p = 0; p < 2 && t + p < seg.hi; ++p, ++v) {
           const int vs = v % kVStages;
-          const uint32_t ph = (v / kVStages) & 1;
-          if (!(ok = wait_w<false>(&bars->vfull[vs], ph, abort_flag)) ||
-              !(ok = wait_w<true>(&bars->peer_v[vs], ph, abort_flag)))
-            return false;
+          if (!(ok = wait_w(&bars->vfull[vs], (v / kVStages) & 1, abort_flag))) break;
           tc_fence_after();
-          const uint64_t a0 = pd + uint64_t((p * 64) >> 4);
+          const uint64_t a0 = pd + uint64_t((uint32_t(vs) * kChunk) >> 4);
           const uint64_t b0 = vd + uint64_t((uint32_t(vs) * kVBytes) >> 4);
-          const bool fresh = t == lo && p == 0;
+          const bool fresh = t == seg.lo && p == 0;
 #pragma unroll
           for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -371,228 +446,248 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
 #pragma unroll
               for (int h = 0; h < 2; ++h)
                 mma_f8_ss_pair_w(tmem + kColO + uint32_t(h) * 128u,
-                                 a0 + uint64_t((term * kChunk + k * 32) >> 4),
-                                 b0 + uint64_t((h * kChunk + k * 32 * 128) >> 4), kIdescPV,
+                                 a0 + uint64_t((term * 64 + k * 32) >> 4),
+                                 b0 + uint64_t((h * kChunk + k * 32 * 128) >> 4),
+                                 term ? kIdescPV | kE5m2A : kIdescPV,
                                  !(fresh && k == 0 && term == 0));
           mma_commit_pair_w(&bars->vempty[vs]);
         }
-        mma_commit_pair_w(&bars->pv_done);
+        if (!ok) break;
+        mma_commit_pair_w(&bars->pv_done[i & 1]);
       }
-      ++seg;
-      return true;
-    });
+    }
     mma_commit_pair_w(&bars->pv_drain);
     volatile int no_abort = 0;
-    wait_w<true>(&bars->pv_drain, 0, &no_abort);
-  } else if (warp == 5 || warp == 6) {
+    wait_w(&bars->pv_drain, 0, &no_abort);
+  } else if (warp == kQkWarp || warp == kPvWarp) {
     // ------------------------------------------------- landed loads, to the leader
     uint32_t n = 0;
-    const bool k_side = warp == 5;
-    for_each_segment(tp, u0, u1, [&](int, int64_t lo, int64_t hi, int64_t) {
-      for (int64_t t = lo; t < hi; t += k_side ? 2 : 1, ++n) {
+    const bool k_side = warp == kQkWarp;
+    while (ok && seg.next()) {
+      for (int64_t t = seg.lo; t < seg.hi; t += k_side ? 2 : 1, ++n) {
         uint64_t* full = k_side ? &bars->kfull[n & 1] : &bars->vfull[n % kVStages];
-        uint64_t* peer = k_side ? &bars->peer_k[n & 1] : &bars->peer_v[n % kVStages];
         const uint32_t ph = (k_side ? n >> 1 : n / kVStages) & 1;
-        if (!(ok = wait_w<false>(full, ph, abort_flag))) return false;
-        if (lane == 0) mbar_arrive_cluster(cluster_map(peer, 0));
+        if (!(ok = wait_w(full, ph, abort_flag))) break;
+        if (lane == 0) mbar_arrive_cluster(cluster_map(full, 0));
         __syncwarp();
       }
-      return true;
-    });
+    }
     // The leader's last arrival on this CTA's barriers.
     volatile int no_abort = 0;
-    wait_w<true>(k_side ? &bars->qk_drain : &bars->pv_drain, 0, &no_abort);
+    wait_w(k_side ? &bars->qk_drain : &bars->pv_drain, 0, &no_abort);
   } else {
     // ------------------------------------------------------------ softmax
-    const int tid = threadIdx.x;             // 0..127
-    const int row = tid & 63, pg = tid >> 6; // head row; page of the pair
+    const int tid = threadIdx.x;             // 0..255
+    const int quad = warp & 3, part = warp >> 2;   // tensor-memory lanes; which half of the columns
+    const int row = (32 * quad + lane) & 63, pg = quad >> 1;   // head row; page of the pair
     const int head = g * kHeadsPerCta + row;
-    const uint32_t lanes = tmem + (uint32_t(32 * warp) << 16);
+    const uint32_t lanes = tmem + (uint32_t(32 * quad) << 16);
     float* s_max = reinterpret_cast<float*>(smem + kOffMax);
     float* s_row = reinterpret_cast<float*>(smem + kOffRowScale);
-    const uint32_t a_q = cluster_map(&bars->q_ready, 0), a_p = cluster_map(&bars->p_full, 0),
+    const uint32_t a_q = cluster_map(&bars->q_ready, 0), a_p0 = cluster_map(&bars->p_full[0], 0),
+                   a_p1 = cluster_map(&bars->p_full[1], 0),
                    a_o = cluster_map(&bars->o_free, 0), a_s0 = cluster_map(&bars->s_free[0], 0),
                    a_s1 = cluster_map(&bars->s_free[1], 0);
-    uint32_t i = 0, v = 0, n_meet = 0;
+    uint32_t i = 0, v = 0;
     auto arrive = [&](uint32_t addr) {
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(addr);
     };
-    // The four warps meet (bounded, unlike a named barrier).
+    // The softmax warps meet.  This wait has no limit of its own, so a warp that
+    // has given up does not leave: it walks on without waiting for anything
+    // else, and every warp comes to every meeting.
+    auto meet_all = [&] {
+      asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
+    };
+    // The four warps that share rows (both pages, both parts of 32 rows).
     auto meet = [&] {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->meet);
-      return ok = wait_w<false>(&bars->meet, n_meet++ & 1, abort_flag);
+      asm volatile("bar.sync %0, %1;" ::"r"(2 + (warp & 1)), "n"(kSoftmaxThreads / 2) : "memory");
+    };
+    auto await = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = wait_w(bar, parity, abort_flag);
+      if (!ok && lane == 0) raise_abort(bars, status);
     };
 
-    // Splits the query block of sequence b into E4M3 terms: a warp takes 16
-    // rows, 4 at a time (their loads are in flight together).
+    // Splits the query block of sequence b into E4M3 terms: a warp takes 8
+    // rows, all loads in flight at once; the code is one row's (the loop stays
+    // rolled: unrolled, fetching its instructions took 10 us at every start).
     auto write_query = [&](int b) {
+      uint4 u[8][2], ur[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const int h = g * kHeadsPerCta + 8 * warp + r;
+        const uint4* src = reinterpret_cast<const uint4*>(q_cat + (int64_t(b) * H + h) * R);
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        u[r][0] = h < H ? src[lane] : z;
+        u[r][1] = h < H ? src[lane + 32] : z;
+        ur[r] = kDr && h < H && lane < kDr / 8 ? src[64 + lane] : z;
+      }
 #pragma unroll 1
-      for (int r0 = 16 * warp; r0 < 16 * warp + 16; r0 += 4) {
-        uint4 u[4][3];
+      for (int r = 0; r < 8; ++r) {
+        const int qr = 8 * warp + r;
+        const uint4 v0 = u[0][0], v1 = u[0][1], vr = ur[0];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int h = g * kHeadsPerCta + r0 + r;
-          const uint4* src = reinterpret_cast<const uint4*>(q_cat + (int64_t(b) * H + h) * R);
-          const uint4 z = make_uint4(0, 0, 0, 0);
-          u[r][0] = h < H ? src[lane] : z;
-          u[r][1] = h < H ? src[lane + 32] : z;
-          u[r][2] = kDr && h < H && lane < kDr / 8 ? src[64 + lane] : z;
+        for (int e = 0; e < 7; ++e) u[e][0] = u[e + 1][0], u[e][1] = u[e + 1][1], ur[e] = ur[e + 1];
+        const uint32_t wd[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        // Largest magnitude of the row: bf16 bits order like their magnitudes.
+        uint32_t top = 0;
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          top = max(top, max(wd[x] & 0x7FFFu, (wd[x] >> 16) & 0x7FFFu));
+        top = __reduce_max_sync(0xffffffffu, top);
+        // Smallest k with top <= 448 * 2^k = 1.75 * 2^(8 + k), kept where 2^k and
+        // 2^-k are normal: top = m 2^(e - 127), 7 mantissa bits, m <= 1.75 up to 96 / 128.
+        const int k = min(max(int(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 96u), -120), 120);
+        const float inv = __uint_as_float(uint32_t(127 - k) << 23);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float a = __uint_as_float(wd[4 * e + x] << 16) * inv;
+            const float c = __uint_as_float(wd[4 * e + x] & 0xFFFF0000u) * inv;
+            hi[x] = e4m3x2(a, c);
+            const float2 back = from_e4m3x2(hi[x]);
+            lo[x] = e4m3x2(a - back.x, c - back.y);
+          }
+          const int un = lane + 32 * e;    // 8 codes: half of 16-byte unit (un % 16) / 2
+          const int off = (un / 16) * kChunk + qr * 128 + ((((un % 16) >> 1) ^ (qr & 7)) * 16) +
+                          (un & 1) * 8;
+          *reinterpret_cast<uint2*>(smem + kOffQ + off) =
+              make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+          *reinterpret_cast<uint2*>(smem + kOffQ + 4 * kChunk + off) =
+              make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
         }
+        if (kDr && lane < kDr / 8) {
+          const uint32_t rd[4] = {vr.x, vr.y, vr.z, vr.w};
+          uint32_t o[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int qr = r0 + r;
-          float f[2][8], top = 0.f;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t wd[4] = {u[r][e].x, u[r][e].y, u[r][e].z, u[r][e].w};
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              f[e][2 * x] = __uint_as_float(wd[x] << 16);
-              f[e][2 * x + 1] = __uint_as_float(wd[x] & 0xFFFF0000u);
-              top = fmaxf(top, fmaxf(fabsf(f[e][2 * x]), fabsf(f[e][2 * x + 1])));
-            }
+          for (int x = 0; x < 4; ++x) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(rd[x] << 16) * inv,
+                                                           __uint_as_float(rd[x] & 0xFFFF0000u) * inv);
+            o[x] = *reinterpret_cast<const uint32_t*>(&p);
           }
-          top = warp_max(top);
-          // Smallest k with top <= 448 * 2^k; kept where 2^k and 2^-k are normal.
-          int k = 0;
-          if (top > 0.f) {
-            const float m = frexpf(top, &k);
-            k = min(max(m <= 0.875f ? k - 9 : k - 8, -120), 120);
-          }
-          const float inv = ldexpf(1.f, -k);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float a = f[e][2 * x] * inv, c = f[e][2 * x + 1] * inv;
-              hi[x] = e4m3x2(a, c);
-              const float2 back = from_e4m3x2(hi[x]);
-              lo[x] = e4m3x2(a - back.x, c - back.y);
-            }
-            const int un = lane + 32 * e;    // 8 codes: half of 16-byte unit (un % 16) / 2
-            const int off = (un / 16) * kChunk + qr * 128 + ((((un % 16) >> 1) ^ (qr & 7)) * 16) +
-                            (un & 1) * 8;
-            *reinterpret_cast<uint2*>(smem + kOffQ + off) =
-                make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-            *reinterpret_cast<uint2*>(smem + kOffQ + 4 * kChunk + off) =
-                make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-          }
-          if (kDr && lane < kDr / 8) {
-            const uint32_t wd[4] = {u[r][2].x, u[r][2].y, u[r][2].z, u[r][2].w};
-            uint32_t o[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const __nv_bfloat162 p = __floats2bfloat162_rn(
-                  __uint_as_float(wd[x] << 16) * inv, __uint_as_float(wd[x] & 0xFFFF0000u) * inv);
-              o[x] = *reinterpret_cast<const uint32_t*>(&p);
-            }
-            *reinterpret_cast<uint4*>(smem + kOffQ + 8 * kChunk + qr * 128 +
-                                      ((lane ^ (qr & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
-          }
-          if (lane == 0) s_row[qr] = ldexpf(1.f, k);
+          *reinterpret_cast<uint4*>(smem + kOffQ + 8 * kChunk + qr * 128 +
+                                    ((lane ^ (qr & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
+        if (lane == 0) s_row[qr] = __uint_as_float(uint32_t(127 + k) << 23);
       }
       fence_proxy_async_smem();
       arrive(a_q);
     };
 
-    const int first_b = tp.next_sequence(-1, u0, u1);
-    if (first_b >= 0) write_query(first_b);
-    for_each_segment(tp, u0, u1, [&](int b, int64_t lo, int64_t hi, int64_t L) {
-      if (!meet()) return false;                       // every row's factor is written
+    bool more = seg.next();
+    if (more) write_query(seg.cur);
+    while (more) {
+      const int b = seg.cur;
+      const int64_t lo = seg.lo, hi = seg.hi, L = seg.L;
+      PageWalk walk(pm, page_scales, b, lo, hi);
+      meet_all();                                      // every row's factor is written
       const float row_scale = s_row[row] * scale_log2;
       float ref = 0.f, top = -INFINITY, l_sum = 0.f;   // ref: set by the first tile
       for (int64_t t = lo; t < hi; t += 2, ++i) {
         const int sb = i & 1;
-        if (!(ok = wait_w<true>(&bars->s_full[sb], (i >> 1) & 1, abort_flag))) return false;
+        await(&bars->s_full[sb], (i >> 1) & 1);
         tc_fence_after();
-        uint32_t x0[32], x1[32];
-        tmem_ld32(lanes + kColS + uint32_t(sb) * 64u, x0);
-        tmem_ld32(lanes + kColS + uint32_t(sb) * 64u + 32u, x1);
-        if (!(ok = wait_w<false>(&bars->sc_full[i & 3], (i >> 2) & 1, abort_flag))) return false;
-        const float sc = bars->scale[i & 3][pg];
+        uint32_t x[32];          // keys 32 part .. of the page
+        tmem_ld32(lanes + kColS + uint32_t(sb) * 64u + uint32_t(part) * 32u, x);
+        int64_t unused;
+        float sc;                // the page's scale (1 where there is no page)
+        walk.at(t + pg, &unused, &sc);
         tmem_wait_ld();
         tc_fence_before();
         arrive(sb ? a_s1 : a_s0);
 
         const int64_t left = t + pg < hi ? L - (t + pg) * kTileKeys : 0;
-        const int valid = int(min(left, int64_t(kTileKeys)));
-        if (valid < kTileKeys) {
+        const int valid = int(min(left, int64_t(kTileKeys))) - 32 * part;
+        if (valid < 32) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (j >= valid) x0[j] = 0xFF800000u;        // -inf
-            if (j + 32 >= valid) x1[j] = 0xFF800000u;
-          }
+          for (int j = 0; j < 32; ++j)
+            if (j >= valid) x[j] = 0xFF800000u;        // -inf
         }
-        float mx = -INFINITY;
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          mx = fmaxf(mx, fmaxf(__uint_as_float(x0[j]), __uint_as_float(x1[j])));
+        for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(x[j]));
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         const float f = row_scale * sc, lsc = log2f(sc);
         float mt = mx * f + lsc;                        // log2 of the largest p * scale
-        s_max[(sb * 2 + pg) * 64 + row] = mt;
-        if (!meet()) return false;
-        mt = fmaxf(mt, s_max[(sb * 2 + (pg ^ 1)) * 64 + row]);
+        float* s_part = s_max + sb * 4 * 64 + row;      // [4 parts][64 rows]
+        s_part[(2 * pg + part) * 64] = mt;
+        meet();
+        mt = fmaxf(fmaxf(s_part[0], s_part[64]), fmaxf(s_part[128], s_part[192]));
 
         float alpha = 1.f;
         if (t == lo) {
-          ref = top = mt;
+          top = mt;
+          ref = mt + kLeadFirst;
         } else {
           top = fmaxf(top, mt);
           const float to = fmaxf(mt, top - kTopWindow);
-          if (to > ref + kRise || to < ref - kFall) {
-            alpha = ex2_approx(ref - to);
-            ref = to;
+          const bool up = to > ref + kRise;
+          if (up || to < ref - kFall) {
+            const float next = to + (up ? kLeadUp : kLeadDown);
+            alpha = ex2_approx(ref - next);
+            ref = next;
             l_sum *= alpha;
           }
         }
         const float shift = lsc + kPScale - ref;
-        float sum = 0.f;
-        uint32_t hi8[16], lo8[16];
-        auto split4 = [&](const uint32_t* s, uint32_t* h, uint32_t* l) {
-          float p[4], q[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = ex2_approx(fmaf(__uint_as_float(s[e]), f, shift));
-            sum += p[e];
-            q[e] = __uint_as_float((__float_as_uint(p[e]) + 0x00080000u) & 0xFFF00000u);
-          }
-          *h = e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16);
-          *l = e4m3x2(p[0] - q[0], p[1] - q[1]) | (e4m3x2(p[2] - q[2], p[3] - q[3]) << 16);
-        };
+        // p = 2^(s f + shift), as hi (E4M3) + lo (E5M2), through fp16.
+        float2 sum2 = make_float2(0.f, 0.f);
+        uint32_t hi8[8], lo8[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          split4(x0 + 4 * j, hi8 + j, lo8 + j);
-          split4(x1 + 4 * j, hi8 + 8 + j, lo8 + 8 + j);
+          uint32_t h[2], l[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 z = fma2(make_float2(__uint_as_float(x[4 * j + 2 * e]),
+                                              __uint_as_float(x[4 * j + 2 * e + 1])),
+                                  make_float2(f, f), make_float2(shift, shift));
+            const float2 p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+            sum2 = add2(sum2, p);
+            const __half2 p16 = __floats2half2_rn(p.x, p.y);
+            h[e] = __nv_cvt_halfraw2_to_fp8x2(p16, __NV_SATFINITE, __NV_E4M3);
+            const __half2 back(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(h[e]), __NV_E4M3));
+            l[e] = __nv_cvt_halfraw2_to_fp8x2(__hsub2(p16, back), __NV_SATFINITE, __NV_E5M2);
+          }
+          hi8[j] = h[0] | (h[1] << 16);
+          lo8[j] = l[0] | (l[1] << 16);
         }
+        const float sum = sum2.x + sum2.y;
         l_sum = fmaf(sum, 1.f / sc, l_sum);
 
-        // P(i - 1) has been read and O holds its product.
-        if (i > 0 && !(ok = wait_w<true>(&bars->pv_done, (i - 1) & 1, abort_flag))) return false;
-        tc_fence_after();
         if (t != lo && __any_sync(0xffffffffu, alpha != 1.f)) {
+          await(&bars->pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1);   // O holds P.C(i - 1)
+          tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < 256; c += 32) {
-            uint32_t r[32];
-            tmem_ld32(lanes + kColO + uint32_t(c), r);
+          for (int c = 128 * part; c < 128 * part + 128; c += 64) {
+            uint32_t r[2][32];
+            tmem_ld32(lanes + kColO + uint32_t(c), r[0]);
+            tmem_ld32(lanes + kColO + uint32_t(c) + 32u, r[1]);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-            tmem_st32(lanes + kColO + uint32_t(c), r);
+            for (int e = 0; e < 64; ++e)
+              r[e / 32][e % 32] = __float_as_uint(__uint_as_float(r[e / 32][e % 32]) * alpha);
+            tmem_st32(lanes + kColO + uint32_t(c), r[0]);
+            tmem_st32(lanes + kColO + uint32_t(c) + 32u, r[1]);
           }
           tmem_wait_st();
         }
-        uint8_t* prow = smem + kOffP + row * 128;
+        // This thread's page of the pair, if there is one: its P tile is free
+        // once the product that read it last is done.
+        const uint32_t vp = v + uint32_t(pg);
+        const int ps = vp % kVStages;
+        if (t + pg < hi && vp >= kVStages) await(&bars->vempty[ps], (vp / kVStages - 1) & 1);
+        if (t + pg < hi) {
+          uint8_t* prow = smem + kOffP + ps * kChunk + row * 128;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int at = ((pg * 4 + u) ^ (row & 7)) * 16;
-          *reinterpret_cast<uint4*>(prow + at) =
-              make_uint4(hi8[4 * u], hi8[4 * u + 1], hi8[4 * u + 2], hi8[4 * u + 3]);
-          *reinterpret_cast<uint4*>(prow + kChunk + at) =
-              make_uint4(lo8[4 * u], lo8[4 * u + 1], lo8[4 * u + 2], lo8[4 * u + 3]);
+          for (int u = 0; u < 2; ++u) {
+            const int un = part * 2 + u;
+            *reinterpret_cast<uint4*>(prow + (un ^ (row & 7)) * 16) =
+                make_uint4(hi8[4 * u], hi8[4 * u + 1], hi8[4 * u + 2], hi8[4 * u + 3]);
+            *reinterpret_cast<uint4*>(prow + ((un + 4) ^ (row & 7)) * 16) =
+                make_uint4(lo8[4 * u], lo8[4 * u + 1], lo8[4 * u + 2], lo8[4 * u + 3]);
+          }
         }
         // Rows past the sequence's end may hold anything, NaN codes among it:
         // their weight is 0, so they are zeroed in the staged page.
@@ -601,28 +696,28 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
           const int64_t rows = L - (t + p) * kTileKeys;
           if (rows >= kTileKeys) continue;
           const int vs = v % kVStages;
-          if (!(ok = wait_w<false>(&bars->vfull[vs], (v / kVStages) & 1, abort_flag))) return false;
+          await(&bars->vfull[vs], (v / kVStages) & 1);
           uint8_t* stage = smem + kOffV + vs * kVBytes;
-          for (int u = tid; u < (kTileKeys - int(rows)) * 16; u += 128)
+          for (int u = tid; u < (kTileKeys - int(rows)) * 16; u += kSoftmaxThreads)
             *reinterpret_cast<uint4*>(stage + (u & 1) * kChunk + (int(rows) + u / 16) * 128 +
                                       ((u / 2) % 8) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        arrive(a_p);
+        arrive(sb ? a_p1 : a_p0);
       }
       // Every QK^T of this sequence has been read back: load the next query.
-      const int nb = tp.next_sequence(b, u0, u1);
-      if (nb >= 0) write_query(nb);
+      more = seg.next();
+      if (more) write_query(seg.cur);
       // Epilogue: normalised partial output and log-sum-exp.
-      // The two halves' sums meet in the buffer that the last tile did not use
+      // The four parts' sums meet in the buffer that the last tile did not use
       // (some warp may still be reading the other; the next sequence's first
       // meeting frees this one).
-      float* s_sum = s_max + (i & 1) * 2 * 64;
-      s_sum[pg * 64 + row] = l_sum;
-      if (!meet()) return false;
-      const float l_row = l_sum + s_sum[(pg ^ 1) * 64 + row];
-      if (!(ok = wait_w<true>(&bars->pv_done, (i - 1) & 1, abort_flag))) return false;
+      float* s_sum = s_max + (i & 1) * 4 * 64 + row;
+      s_sum[(2 * pg + part) * 64] = l_sum;
+      meet();
+      const float l_row = (s_sum[0] + s_sum[64]) + (s_sum[128] + s_sum[192]);
+      await(&bars->pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1);
       tc_fence_after();
       const float inv = 1.f / l_row;
       const int slot = b + w;
@@ -631,13 +726,13 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
       // combine that reads them next.
       const uint64_t keep = l2_policy_evict_last();
 #pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {
+      for (int c = 128 * part; c < 128 * part + 128; c += 32) {
         uint32_t r[32];
         tmem_ld32(lanes + kColO + uint32_t(c), r);
         tmem_wait_ld();
-        // Accumulator column c of half h = c / 128 is latent column
+        // Accumulator column c of product h = c / 128 is latent column
         // 256 h + 128 pg + c % 128.
-        const int col = (c / 128) * 256 + pg * 128 + c % 128;
+        const int col = part * 256 + pg * 128 + c % 128;
         float* dst = o_part + ((int64_t(slot) * (kDc / 4) + col / 4) * H + head) * 4;
         if (head < H) {
 #pragma unroll
@@ -650,12 +745,11 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
                               keep);
         }
       }
-      if (pg == 0 && head < H)
+      if (pg == 0 && part == 0 && head < H)
         lse_part[int64_t(slot) * H + head] = (log2f(l_row) + ref - kPScale) * 0.69314718055994531f;
       tc_fence_before();
       arrive(a_o);
-      return true;
-    });
+    }
   }
   if (!ok && lane == 0) raise_abort(bars, status);
 
@@ -663,17 +757,17 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
   // shared memory is released (after a give-up some were never waited for), and
   // neither CTA leaves while the other's products may still read from it.
   __syncwarp();
-  if (lane == 0 && (warp == 4 || warp == 7)) {
+  if (lane == 0 && (warp == kKWarp || warp == kVWarp)) {
     volatile int no_abort = 0;
-    const uint32_t n_st = warp == 4 ? kKStages : kVStages;
+    const uint32_t n_st = warp == kKWarp ? kKStages : kVStages;
     for (uint32_t k = (n_issued > n_st ? n_issued - n_st : 0); k < n_issued; ++k)
-      mbar_wait(warp == 4 ? &bars->kfull[k % n_st] : &bars->vfull[k % n_st], (k / n_st) & 1,
-                &no_abort, kWaitLimitCycles);
+      mbar_wait(warp == kKWarp ? &bars->kfull[k % n_st] : &bars->vfull[k % n_st], (k / n_st) & 1,
+                &no_abort, kWaitLimitCycles / 100);
   }
   tc_fence_before();
   __syncthreads();
   cluster_sync();
-  if (warp == 5) {
+  if (warp == kQkWarp) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
   }
