@@ -149,12 +149,14 @@ struct Segments {
   const int32_t* seqlens;
   int B, b;             // b: the sequence after the current one
   int64_t cap, pre, u0, u1;
+  int32_t len_b;        // its length, read ahead
   int cur;              // the current sequence, its tiles [lo, hi) and length
   int64_t lo, hi, L;
   __device__ bool next() {
     while (b < B && pre < u1) {
       cur = b++;
-      L = clamp_len(seqlens[cur], cap);
+      L = clamp_len(len_b, cap);
+      if (b < B) len_b = seqlens[b];
       const int64_t nt = tiles_of(L), r0 = pre + kSwitchUnits;
       if (nt == 0) continue;
       pre = r0 + nt;
@@ -166,28 +168,33 @@ struct Segments {
   }
 };
 
-// All threads; `scratch` is shared memory for kThreads / 32 + 2 values.  False
+// All threads; `scratch` is shared memory for kThreads / 32 + 3 values.  False
 // if the worker has no units.
 __device__ __forceinline__ bool find_segments(const int32_t* seqlens, int B, int64_t cap, int w,
                                               int W, int64_t* scratch, Segments* out) {
   constexpr int kWarps = kThreads / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t sum = 0;
-  for (int b = threadIdx.x; b < B; b += kThreads) sum += units_of(clamp_len(seqlens[b], cap));
+  const int32_t len0 = int(threadIdx.x) < B ? seqlens[threadIdx.x] : 0;
+  int64_t sum = units_of(clamp_len(len0, cap));
+  for (int b = threadIdx.x + kThreads; b < B; b += kThreads)
+    sum += units_of(clamp_len(seqlens[b], cap));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) scratch[warp] = sum;
   __syncthreads();
   int64_t total = 0;
+#pragma unroll
   for (int k = 0; k < kWarps; ++k) total += scratch[k];
   __syncthreads();
   const int64_t u0 = worker_tile_begin(w, total, W), u1 = worker_tile_begin(w + 1, total, W);
   if (u0 >= u1) return false;
   // The sequence that unit u0 belongs to, kThreads of them at a time.
   int64_t base = 0;
+#pragma unroll 1
   for (int b0 = 0;; b0 += kThreads) {
     const int b = b0 + int(threadIdx.x);
-    const int64_t n = b < B ? units_of(clamp_len(seqlens[b], cap)) : 0;
+    const int32_t len = b0 == 0 ? len0 : b < B ? seqlens[b] : 0;
+    const int64_t n = b < B ? units_of(clamp_len(len, cap)) : 0;
     int64_t e = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -197,17 +204,21 @@ __device__ __forceinline__ bool find_segments(const int32_t* seqlens, int B, int
     if (lane == 31) scratch[warp] = e;
     __syncthreads();
     int64_t chunk = 0;
+#pragma unroll
     for (int k = 0; k < kWarps; ++k) {
       if (k < warp) e += scratch[k];
       chunk += scratch[k];
     }
     e += base;
-    if (u0 < e && u0 >= e - n) scratch[kWarps] = b, scratch[kWarps + 1] = e - n;
+    if (u0 < e && u0 >= e - n)
+      scratch[kWarps] = b, scratch[kWarps + 1] = e - n, scratch[kWarps + 2] = len;
     __syncthreads();
     base += chunk;
     if (u0 < base) break;      // u0 < total, so some chunk holds it
   }
-  *out = Segments{seqlens, B, int(scratch[kWarps]), cap, scratch[kWarps + 1], u0, u1, 0, 0, 0, 0};
+  *out = Segments{seqlens, B,  int(scratch[kWarps]),         cap, scratch[kWarps + 1],
+                  u0,      u1, int32_t(scratch[kWarps + 2]), 0,   0,
+                  0,       0};
   __syncthreads();             // before the scratch is used for anything else
   return true;
 }
@@ -280,11 +291,6 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
   const int g = blockIdx.x, w = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  pdl_wait();
-  Segments seg;
-  // False: the same in both CTAs of a pair.
-  if (!find_segments(seqlens, B, cap, w, W, reinterpret_cast<int64_t*>(smem), &seg)) return;
-
   if (threadIdx.x == 0) {
     // The leader's also wait for the other CTA's word that its stage has landed.
     const uint32_t n_full = rank == 0 ? 2 : 1;
@@ -319,10 +325,16 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort_flag;
+
+  pdl_wait();     // everything above is independent of what earlier kernels write
+  Segments seg;
+  const bool busy = find_segments(seqlens, B, cap, w, W, reinterpret_cast<int64_t*>(smem), &seg);
   uint32_t n_issued = 0;     // K or V stages that this producer warp has loaded into
   bool ok = true;
 
-  if (warp == kKWarp) {
+  if (!busy) {
+    // No units: the same in both CTAs of the pair.
+  } else if (warp == kKWarp) {
     // ------------------------------------------------------------ K and scales
     uint32_t i = 0;
     while (ok && seg.next()) {
@@ -509,7 +521,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
     };
 
     // Splits the query block of sequence b into E4M3 terms: a warp takes 8
-    // rows, all loads in flight at once; the code is one row's (the loop stays
+    // rows, all loads in flight at once; the code is two rows' (the loop stays
     // rolled: unrolled, fetching its instructions took 10 us at every start).
     auto write_query = [&](int b) {
       uint4 u[8][2], ur[8];
@@ -523,54 +535,67 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
         ur[r] = kDr && h < H && lane < kDr / 8 ? src[64 + lane] : z;
       }
 #pragma unroll 1
-      for (int r = 0; r < 8; ++r) {
-        const int qr = 8 * warp + r;
-        const uint4 v0 = u[0][0], v1 = u[0][1], vr = ur[0];
+      for (int r0 = 0; r0 < 8; r0 += 2) {
+        uint32_t wd[2][8], rd[2][4], top[2] = {0, 0};
+        float inv[2];
 #pragma unroll
-        for (int e = 0; e < 7; ++e) u[e][0] = u[e + 1][0], u[e][1] = u[e + 1][1], ur[e] = ur[e + 1];
-        const uint32_t wd[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-        // Largest magnitude of the row: bf16 bits order like their magnitudes.
-        uint32_t top = 0;
+        for (int r = 0; r < 2; ++r) {
+          const uint4 v0 = u[r][0], v1 = u[r][1], vr = ur[r];
+          wd[r][0] = v0.x, wd[r][1] = v0.y, wd[r][2] = v0.z, wd[r][3] = v0.w;
+          wd[r][4] = v1.x, wd[r][5] = v1.y, wd[r][6] = v1.z, wd[r][7] = v1.w;
+          rd[r][0] = vr.x, rd[r][1] = vr.y, rd[r][2] = vr.z, rd[r][3] = vr.w;
+          // Largest magnitude of the row: bf16 bits order like their magnitudes.
 #pragma unroll
-        for (int x = 0; x < 8; ++x)
-          top = max(top, max(wd[x] & 0x7FFFu, (wd[x] >> 16) & 0x7FFFu));
-        top = __reduce_max_sync(0xffffffffu, top);
-        // Smallest k with top <= 448 * 2^k = 1.75 * 2^(8 + k), kept where 2^k and
-        // 2^-k are normal: top = m 2^(e - 127), 7 mantissa bits, m <= 1.75 up to 96 / 128.
-        const int k = min(max(int(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 96u), -120), 120);
-        const float inv = __uint_as_float(uint32_t(127 - k) << 23);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float a = __uint_as_float(wd[4 * e + x] << 16) * inv;
-            const float c = __uint_as_float(wd[4 * e + x] & 0xFFFF0000u) * inv;
-            hi[x] = e4m3x2(a, c);
-            const float2 back = from_e4m3x2(hi[x]);
-            lo[x] = e4m3x2(a - back.x, c - back.y);
-          }
-          const int un = lane + 32 * e;    // 8 codes: half of 16-byte unit (un % 16) / 2
-          const int off = (un / 16) * kChunk + qr * 128 + ((((un % 16) >> 1) ^ (qr & 7)) * 16) +
-                          (un & 1) * 8;
-          *reinterpret_cast<uint2*>(smem + kOffQ + off) =
-              make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-          *reinterpret_cast<uint2*>(smem + kOffQ + 4 * kChunk + off) =
-              make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+          for (int x = 0; x < 8; ++x)
+            top[r] = max(top[r], max(wd[r][x] & 0x7FFFu, (wd[r][x] >> 16) & 0x7FFFu));
         }
-        if (kDr && lane < kDr / 8) {
-          const uint32_t rd[4] = {vr.x, vr.y, vr.z, vr.w};
-          uint32_t o[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(rd[x] << 16) * inv,
-                                                           __uint_as_float(rd[x] & 0xFFFF0000u) * inv);
-            o[x] = *reinterpret_cast<const uint32_t*>(&p);
-          }
-          *reinterpret_cast<uint4*>(smem + kOffQ + 8 * kChunk + qr * 128 +
-                                    ((lane ^ (qr & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int e = 0; e < 6; ++e) u[e][0] = u[e + 2][0], u[e][1] = u[e + 2][1], ur[e] = ur[e + 2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          top[r] = __reduce_max_sync(0xffffffffu, top[r]);
+          // Smallest k with top <= 448 * 2^k = 1.75 * 2^(8 + k), kept where 2^k and
+          // 2^-k are normal: top = m 2^(e - 127), 7 mantissa bits, m <= 1.75 up to 96 / 128.
+          const int k =
+              min(max(int(top[r] >> 7) - 127 - 8 + ((top[r] & 0x7Fu) > 96u), -120), 120);
+          inv[r] = __uint_as_float(uint32_t(127 - k) << 23);
+          if (lane == 0) s_row[8 * warp + r0 + r] = __uint_as_float(uint32_t(127 + k) << 23);
         }
-        if (lane == 0) s_row[qr] = __uint_as_float(uint32_t(127 + k) << 23);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int qr = 8 * warp + r0 + r;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float a = __uint_as_float(wd[r][4 * e + x] << 16) * inv[r];
+              const float c = __uint_as_float(wd[r][4 * e + x] & 0xFFFF0000u) * inv[r];
+              hi[x] = e4m3x2(a, c);
+              const float2 back = from_e4m3x2(hi[x]);
+              lo[x] = e4m3x2(a - back.x, c - back.y);
+            }
+            const int un = lane + 32 * e;    // 8 codes: half of 16-byte unit (un % 16) / 2
+            const int off = (un / 16) * kChunk + qr * 128 + ((((un % 16) >> 1) ^ (qr & 7)) * 16) +
+                            (un & 1) * 8;
+            *reinterpret_cast<uint2*>(smem + kOffQ + off) =
+                make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+            *reinterpret_cast<uint2*>(smem + kOffQ + 4 * kChunk + off) =
+                make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+          }
+          if (kDr && lane < kDr / 8) {
+            uint32_t o[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const __nv_bfloat162 p =
+                  __floats2bfloat162_rn(__uint_as_float(rd[r][x] << 16) * inv[r],
+                                        __uint_as_float(rd[r][x] & 0xFFFF0000u) * inv[r]);
+              o[x] = *reinterpret_cast<const uint32_t*>(&p);
+            }
+            *reinterpret_cast<uint4*>(smem + kOffQ + 8 * kChunk + qr * 128 +
+                                      ((lane ^ (qr & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
       }
       fence_proxy_async_smem();
       arrive(a_q);
@@ -582,6 +607,14 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
       const int b = seg.cur;
       const int64_t lo = seg.lo, hi = seg.hi, L = seg.L;
       PageWalk walk(pm, page_scales, b, lo, hi);
+      if (tid == 0) {      // the next sequence's query block into L2 ahead of its use
+        Segments ahead = seg;
+        if (ahead.next()) {
+          const int64_t r0 = int64_t(ahead.cur) * H + g * kHeadsPerCta;
+          const int rows = min(H - g * kHeadsPerCta, kHeadsPerCta);
+          if (rows > 0) bulk_prefetch_l2(q_cat + r0 * R, uint32_t(rows * R * 2));
+        }
+      }
       meet_all();                                      // every row's factor is written
       const float row_scale = s_row[row] * scale_log2;
       float ref = 0.f, top = -INFINITY, l_sum = 0.f;   // ref: set by the first tile
