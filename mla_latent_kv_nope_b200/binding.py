@@ -8,6 +8,7 @@ library raises immediately -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -63,6 +64,10 @@ class RopeTable(ctypes.Structure):
                 ("amplitude", ctypes.c_float), ("reserved", ctypes.c_int32),
                 ("turn", ctypes.c_uint64 * 128)]
 
+    @property
+    def address(self) -> int:
+        return ctypes.addressof(self)
+
 
 @dataclass(frozen=True)
 class Dims:
@@ -80,6 +85,14 @@ class Dims:
     def c(self) -> CDims:
         return CDims(self.B, self.H, self.d_c, self.d_r, self.d_nope, self.d_v,
                      self.cache_capacity, MLA_BF16 if self.dtype == "bf16" else MLA_F32)
+
+    @functools.cached_property
+    def ref(self):
+        """A reference to the C struct, made once (the fields are frozen)."""
+        return ctypes.byref(self.c())
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "ref"}
 
     @property
     def torch_dtype(self):
@@ -168,17 +181,19 @@ def _ptr(t):
         raise TypeError("expected a torch tensor")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream=None):
+    """Raw handle of the given stream, or of the current one of the current device."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        torch.cuda.init()       # a host without a GPU raises here
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _need(t, dtype, shape, name):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_cuda:
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda:
         raise ValueError(f"{name}: expected CUDA {dtype} {tuple(shape)}, got "
                          f"{t.device} {t.dtype} {tuple(t.shape)}")
 
@@ -199,7 +214,7 @@ def cache_row_elems(d_c: int, d_r: int) -> int:
 
 def cache_append_workspace_bytes(dims: Dims, hidden: int) -> int:
     """Bytes of fp32 workspace mla_cache_append needs for this hidden size."""
-    return int(load_library().mla_cache_append_workspace_bytes(ctypes.byref(dims.c()), hidden))
+    return int(load_library().mla_cache_append_workspace_bytes(dims.ref, hidden))
 
 
 def cache_append(dims: Dims, h, W_DKV, gamma, cache, seqlens, workspace, eps=1e-6,
@@ -216,7 +231,7 @@ def cache_append(dims: Dims, h, W_DKV, gamma, cache, seqlens, workspace, eps=1e-
         _need(gamma, torch.float32, (dims.d_c,), "gamma")
     _need_ws(workspace)
     st = load_library().mla_cache_append(
-        ctypes.byref(dims.c()), hidden, _ptr(h), _ptr(W_DKV), _ptr(gamma), eps, rope_base,
+        dims.ref, hidden, _ptr(h), _ptr(W_DKV), _ptr(gamma), eps, rope_base,
         _ptr(cache), _ptr(seqlens), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream))
     _check("mla_cache_append", st)
@@ -245,7 +260,7 @@ def cache_append_paged(dims: Dims, h, W_DKV, gamma, cache_pool, block_table, seq
         _need(gamma, torch.float32, (dims.d_c,), "gamma")
     _need_ws(workspace)
     st = load_library().mla_cache_append_paged(
-        ctypes.byref(dims.c()), hidden, _ptr(h), _ptr(W_DKV), _ptr(gamma), eps, rope_base,
+        dims.ref, hidden, _ptr(h), _ptr(W_DKV), _ptr(gamma), eps, rope_base,
         _ptr(cache_pool), cache_pool.shape[0], _ptr(block_table), block_table.shape[1],
         _ptr(seqlens), _ptr(workspace), workspace.numel() * workspace.element_size(),
         _stream(stream))
@@ -261,7 +276,7 @@ def decode_paged(dims: Dims, q_cat, cache_pool, block_table, seqlens, softmax_sc
     _need_ws(workspace)
     used = ctypes.c_int(0)
     st = load_library().mla_decode_paged(
-        ctypes.byref(dims.c()), _ptr(q_cat), _ptr(cache_pool), cache_pool.shape[0],
+        dims.ref, _ptr(q_cat), _ptr(cache_pool), cache_pool.shape[0],
         _ptr(block_table), block_table.shape[1], _ptr(seqlens), float(softmax_scale), num_splits,
         _ptr(workspace), workspace.numel() * workspace.element_size(), ctypes.byref(used),
         _stream(stream))
@@ -294,7 +309,7 @@ def cache_append_fp8(dims: Dims, h, W_DKV, gamma, cache, scales, seqlens, worksp
         _need(gamma, torch.float32, (dims.d_c,), "gamma")
     _need_ws(workspace)
     st = load_library().mla_cache_append_fp8(
-        ctypes.byref(dims.c()), hidden, _ptr(h), _ptr(W_DKV), _ptr(gamma), eps, rope_base,
+        dims.ref, hidden, _ptr(h), _ptr(W_DKV), _ptr(gamma), eps, rope_base,
         _ptr(cache), _ptr(scales), _ptr(seqlens), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream))
     _check("mla_cache_append_fp8", st)
@@ -308,7 +323,7 @@ def decode_fp8(dims: Dims, q_cat, cache, scales, seqlens, softmax_scale, workspa
     _need(seqlens, torch.int32, (dims.B,), "seqlens")
     _need_ws(workspace)
     used = ctypes.c_int(0)
-    st = load_library().mla_decode_fp8(ctypes.byref(dims.c()), _ptr(q_cat), _ptr(cache),
+    st = load_library().mla_decode_fp8(dims.ref, _ptr(q_cat), _ptr(cache),
                                        _ptr(scales), _ptr(seqlens), float(softmax_scale),
                                        num_splits, _ptr(workspace),
                                        workspace.numel() * workspace.element_size(),
@@ -327,7 +342,7 @@ def absorb_q(dims: Dims, q_nope, q_pe, W_UK, q_pos, q_cat, rope_base=10000.0, st
     _need(q_cat, dt, (dims.B, dims.H, dims.R), "q_cat")
     if q_pos is not None:
         _need(q_pos, torch.int32, (dims.B,), "q_pos")
-    st = load_library().mla_absorb_q(ctypes.byref(dims.c()), _ptr(q_nope), _ptr(q_pe),
+    st = load_library().mla_absorb_q(dims.ref, _ptr(q_nope), _ptr(q_pe),
                                      _ptr(W_UK), _ptr(q_pos), rope_base, _ptr(q_cat),
                                      _stream(stream))
     _check("mla_absorb_q", st)
@@ -335,12 +350,12 @@ def absorb_q(dims: Dims, q_nope, q_pe, W_UK, q_pos, q_cat, rope_base=10000.0, st
 
 def decode_default_splits(dims: Dims) -> int:
     """The split count mla_decode uses on the current device when asked for 0."""
-    return int(load_library().mla_decode_default_splits(ctypes.byref(dims.c())))
+    return int(load_library().mla_decode_default_splits(dims.ref))
 
 
 def decode_workspace_bytes(dims: Dims, num_splits: int = 0) -> int:
     """Bytes of workspace mla_decode needs for this many splits (0 = default)."""
-    return int(load_library().mla_decode_workspace_bytes(ctypes.byref(dims.c()), num_splits))
+    return int(load_library().mla_decode_workspace_bytes(dims.ref, num_splits))
 
 
 def decode(dims: Dims, q_cat, cache, seqlens, softmax_scale, workspace, num_splits=0,
@@ -353,7 +368,7 @@ def decode(dims: Dims, q_cat, cache, seqlens, softmax_scale, workspace, num_spli
     _need(seqlens, torch.int32, (dims.B,), "seqlens")
     _need_ws(workspace)
     used = ctypes.c_int(0)
-    st = load_library().mla_decode(ctypes.byref(dims.c()), _ptr(q_cat), _ptr(cache),
+    st = load_library().mla_decode(dims.ref, _ptr(q_cat), _ptr(cache),
                                    _ptr(seqlens), float(softmax_scale), num_splits,
                                    _ptr(workspace), workspace.numel() * workspace.element_size(),
                                    ctypes.byref(used), _stream(stream))
@@ -369,7 +384,7 @@ def combine(dims: Dims, seqlens, workspace, splits_used, o_lat, lse=None, stream
     _need(o_lat, torch.float32, (dims.B, dims.H, dims.d_c), "o_lat")
     if lse is not None:
         _need(lse, torch.float32, (dims.B, dims.H), "lse")
-    st = load_library().mla_combine(ctypes.byref(dims.c()), _ptr(seqlens), _ptr(workspace),
+    st = load_library().mla_combine(dims.ref, _ptr(seqlens), _ptr(workspace),
                                     workspace.numel() * workspace.element_size(), splits_used,
                                     _ptr(o_lat), _ptr(lse), _stream(stream))
     _check("mla_combine", st)
@@ -385,7 +400,7 @@ def merge_partials(dims: Dims, o_parts, lse_parts, o_lat, lse=None, stream=None)
     _need(o_lat, torch.float32, (dims.B, dims.H, dims.d_c), "o_lat")
     if lse is not None:
         _need(lse, torch.float32, (dims.B, dims.H), "lse")
-    st = load_library().mla_merge_partials(ctypes.byref(dims.c()), n, _ptr(o_parts),
+    st = load_library().mla_merge_partials(dims.ref, n, _ptr(o_parts),
                                            _ptr(lse_parts), _ptr(o_lat), _ptr(lse),
                                            _stream(stream))
     _check("mla_merge_partials", st)
@@ -397,7 +412,7 @@ def out_proj(dims: Dims, o_lat, W_UV, out, stream=None):
     _need(o_lat, torch.float32, (dims.B, dims.H, dims.d_c), "o_lat")
     _need(W_UV, dt, (dims.H, dims.d_v, dims.d_c), "W_UV")
     _need(out, dt, (dims.B, dims.H, dims.d_v), "out")
-    st = load_library().mla_out_proj(ctypes.byref(dims.c()), _ptr(o_lat), _ptr(W_UV), _ptr(out),
+    st = load_library().mla_out_proj(dims.ref, _ptr(o_lat), _ptr(W_UV), _ptr(out),
                                      _stream(stream))
     _check("mla_out_proj", st)
 
@@ -410,7 +425,7 @@ def debug_inject_wait(cycles: int) -> None:
 
 
 def prefill_workspace_bytes(dims: Dims, T: int, L: int) -> int:
-    return int(load_library().mla_prefill_workspace_bytes(ctypes.byref(dims.c()), T, L))
+    return int(load_library().mla_prefill_workspace_bytes(dims.ref, T, L))
 
 
 def prefill(dims: Dims, q_nope, q_pe, q_pos, W_UK, W_UV, rows, out, workspace, lse=None,
@@ -431,7 +446,7 @@ def prefill(dims: Dims, q_nope, q_pe, q_pos, W_UK, W_UV, rows, out, workspace, l
         _need(lse, torch.float32, (T, dims.H), "lse")
     _need_ws(workspace)
     st = load_library().mla_prefill(
-        ctypes.byref(dims.c()), T, L, _ptr(q_nope), _ptr(q_pe) if dims.d_r else None,
+        dims.ref, T, L, _ptr(q_nope), _ptr(q_pe) if dims.d_r else None,
         _ptr(q_pos), _ptr(W_UK), _ptr(W_UV), _ptr(rows), softmax_scale, rope_base, _ptr(out),
         _ptr(lse) if lse is not None else None, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream))
@@ -445,13 +460,13 @@ def fold_output_weights(dims: Dims, W_O, W_UV, W_fold, stream=None):
     _need(W_O, dims.torch_dtype, (d_model, dims.H * dims.d_v), "W_O")
     _need(W_UV, dims.torch_dtype, (dims.H, dims.d_v, dims.d_c), "W_UV")
     _need(W_fold, dims.torch_dtype, (d_model, dims.H * dims.d_c), "W_fold")
-    st = load_library().mla_fold_output_weights(ctypes.byref(dims.c()), d_model, _ptr(W_O),
+    st = load_library().mla_fold_output_weights(dims.ref, d_model, _ptr(W_O),
                                                 _ptr(W_UV), _ptr(W_fold), _stream(stream))
     _check("mla_fold_output_weights", st)
 
 
 def out_proj_folded_workspace_bytes(dims: Dims, d_model: int) -> int:
-    return int(load_library().mla_out_proj_folded_workspace_bytes(ctypes.byref(dims.c()),
+    return int(load_library().mla_out_proj_folded_workspace_bytes(dims.ref,
                                                                   d_model))
 
 
@@ -463,32 +478,59 @@ def out_proj_folded(dims: Dims, o_lat, W_fold, u, workspace, stream=None):
     _need(u, dims.torch_dtype, (dims.B, d_model), "u")
     _need_ws(workspace)
     st = load_library().mla_out_proj_folded(
-        ctypes.byref(dims.c()), d_model, _ptr(o_lat), _ptr(W_fold), _ptr(u), _ptr(workspace),
+        dims.ref, d_model, _ptr(o_lat), _ptr(W_fold), _ptr(u), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream))
     _check("mla_out_proj_folded", st)
 
 
 # ---------------------------------------------------------------------------
 # Paged serving: rotary positions, page plans, writes of many tokens, 8-bit pages.
+# Their kernels take a few microseconds, so these wrappers keep the host's part
+# short: one look at each tensor, raw pointers and streams.
 _ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 _ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+_I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
 
 
-def _same_device(first, *rest):
-    """The device index all CUDA tensors of a call share."""
-    dev = first.device.index
-    for t in rest:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
-    return dev
+def _arg(t, dtype, shape, name, dev):
+    """Device address of a contiguous CUDA tensor of this dtype and shape on device `dev`."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _need(t, dtype, shape, name)
+        raise ValueError(f"tensors on different devices: {name} is on {t.device}, not cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors must be contiguous")
+    return t.data_ptr()
 
 
-def _on(dev, stream, fn, *args):
-    """Call fn(*args, stream) with `dev` current (its current stream unless one is given)."""
-    if torch.cuda.current_device() == dev:
-        return fn(*args, (stream or torch.cuda.current_stream(dev)).cuda_stream)
-    with torch.cuda.device(dev):
-        return fn(*args, (stream or torch.cuda.current_stream(dev)).cuda_stream)
+def _device(t, name):
+    """Device index of a CUDA tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        got = t.device if isinstance(t, torch.Tensor) else type(t).__name__
+        raise ValueError(f"{name}: expected a CUDA tensor, got {got}")
+    return t.get_device()
+
+
+def _ws_arg(t, dev):
+    """Address and bytes of a scratch buffer on device `dev`."""
+    _need_ws(t)
+    if t.get_device() != dev:
+        raise ValueError(f"tensors on different devices: workspace is on {t.device}, not cuda:{dev}")
+    return t.data_ptr(), t.nbytes
+
+
+def _launch(fn, dev, stream, *args):
+    """Call the library's `fn`(*args, stream) with `dev` current, on its current
+    stream unless one is given, and raise on a bad status."""
+    f = getattr(_lib or load_library(), fn)
+    if torch._C._cuda_getDevice() == dev:
+        st = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
+               else stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
+                   else stream.cuda_stream)
+    if st:
+        _check(fn, st)
 
 
 def _table_ptr(table):
@@ -496,16 +538,18 @@ def _table_ptr(table):
         return None
     if not isinstance(table, RopeTable):
         raise TypeError("table must come from rope_table()")
-    return ctypes.addressof(table)
+    return table.address
 
 
-def _need_rows(x, dtype, width, name):
-    """[T, width] rows with unit inner stride (rows of a wider matrix are fine)."""
-    if (not x.is_cuda or x.dtype != dtype or x.dim() != 2 or x.shape[1] != width
+def _rows(x, dtype, width, dev):
+    """Address, rows and row stride of [T, width] rows with unit inner stride (rows of a
+    wider matrix are fine)."""
+    if (x.dtype is not dtype or x.dim() != 2 or x.shape[1] != width
             or (width > 1 and x.stride(1) != 1)):
-        raise ValueError(f"{name}: expected CUDA {dtype} rows [T, {width}] with unit inner "
-                         f"stride, got {x.device} {x.dtype} {tuple(x.shape)} "
-                         f"strides {x.stride()}")
+        raise ValueError(f"x: expected CUDA {dtype} rows [T, {width}] with unit inner stride, "
+                         f"got {x.device} {x.dtype} {tuple(x.shape)} strides {x.stride()}")
+    T = x.shape[0]
+    return x.data_ptr(), T, x.stride(0) if T > 1 else width
 
 
 def rope_table(d_r: int, base: float = 10000.0, layout: str = "half", scaling: str = "none",
@@ -531,28 +575,27 @@ def rope(table: RopeTable, x, pos, out=None, transpose=False, stream=None):
     pos [T] int32 into ``out`` (x itself rotates in place; a new contiguous
     tensor if None).  ``transpose`` applies the transposed rotation (the
     gradient of the rotation's output taken back to its input)."""
-    tab = _table_ptr(table)
-    if tab is None:
+    if not isinstance(table, RopeTable):
         raise TypeError("table must come from rope_table()")
-    if (x.dim() not in (2, 3) or x.shape[-1] != table.d_r or not x.is_cuda
-            or x.dtype not in (torch.bfloat16, torch.float32) or x.stride(-1) != 1):
+    dev = _device(x, "x")
+    shape, st, dt = x.shape, x.stride(), x.dtype
+    n = len(shape)
+    if (n != 3 and n != 2) or shape[-1] != table.d_r or st[-1] != 1 or (dt is not _BF16
+                                                                        and dt is not _F32):
         raise ValueError(f"x: expected CUDA bf16 or fp32 [T, (H,) {table.d_r}] with unit inner "
-                         f"stride, got {x.device} {x.dtype} {tuple(x.shape)} strides {x.stride()}")
-    T = x.shape[0]
-    _need(pos, torch.int32, (T,), "pos")
+                         f"stride, got {x.device} {dt} {tuple(shape)} strides {st}")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape or out.dtype != x.dtype or not out.is_cuda or out.stride(-1) != 1:
-        raise ValueError("out must match x's shape and dtype, with unit inner stride")
-    heads = x.dim() == 3
-    if heads and x.shape[1] == 0:
-        return out
-    dev = _same_device(x, pos, out)
-    st = _on(dev, stream, load_library().mla_rope, MLA_BF16 if x.dtype == torch.bfloat16 else MLA_F32,
-             tab, T, x.shape[1] if heads else 1, x.data_ptr(), x.stride(0),
-             x.stride(1) if heads else 0, _ptr(pos), out.data_ptr(), out.stride(0),
-             out.stride(1) if heads else 0, int(bool(transpose)))
-    _check("mla_rope", st)
+        out = torch.empty(shape, dtype=dt, device=x.device)
+    elif (out.shape != shape or out.dtype is not dt or out.get_device() != dev
+          or out.stride(-1) != 1):
+        raise ValueError("out must match x's shape, dtype and device, with unit inner stride")
+    so = out.stride()
+    T = shape[0]
+    p = _arg(pos, _I32, (T,), "pos", dev)
+    H, xh, oh = (shape[1], st[1], so[1]) if n == 3 else (1, 0, 0)
+    if H:
+        _launch("mla_rope", dev, stream, MLA_BF16 if dt is _BF16 else MLA_F32, table.address, T, H,
+                x.data_ptr(), st[0], xh, p, out.data_ptr(), so[0], oh, 1 if transpose else 0)
     return out
 
 
@@ -568,50 +611,33 @@ def plan_pages(seqlens, new_lens, block_table, free_pages, free_count, num_pages
     list into block_table [B, max_blocks], and fill query_start [B+1],
     positions [T] (int32) and slots [T] (int64); seqlens_out and
     free_count_out may be seqlens and free_count."""
-    B, T = seqlens.shape[0], positions.shape[0]
-    i32 = torch.int32
-    _need(seqlens, i32, (B,), "seqlens")
-    _need(new_lens, i32, (B,), "new_lens")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_blocks]")
-    _need(block_table, i32, (B, block_table.shape[1]), "block_table")
-    _need(free_pages, i32, (free_pages.numel(),), "free_pages")
-    _need(free_count, i32, (1,), "free_count")
-    _need(query_start, i32, (B + 1,), "query_start")
-    _need(positions, i32, (T,), "positions")
-    _need(slots, torch.int64, (T,), "slots")
-    _need(seqlens_out, i32, (B,), "seqlens_out")
-    _need(free_count_out, i32, (1,), "free_count_out")
-    if token_request is not None:
-        _need(token_request, i32, (T,), "token_request")
-    _need_ws(workspace)
-    dev = _same_device(seqlens, new_lens, block_table, free_pages, free_count, query_start,
-                       positions, slots, seqlens_out, free_count_out, workspace, token_request)
-    st = _on(dev, stream, load_library().mla_plan_pages, B, _ptr(seqlens), _ptr(new_lens),
-             _ptr(block_table), block_table.shape[1], _ptr(free_pages), free_pages.shape[0],
-             _ptr(free_count), num_pages, T, _ptr(query_start), _ptr(positions), _ptr(slots),
-             _ptr(token_request), _ptr(seqlens_out), _ptr(free_count_out), _ptr(workspace),
-             workspace.numel() * workspace.element_size())
-    _check("mla_plan_pages", st)
+    dev = _device(seqlens, "seqlens")
+    B, T, F = seqlens.shape[0], positions.shape[0], free_pages.numel()
+    mb = block_table.shape[-1]
+    b, one, t = (B,), (1,), (T,)
+    ws, nws = _ws_arg(workspace, dev)
+    _launch("mla_plan_pages", dev, stream, B, _arg(seqlens, _I32, b, "seqlens", dev),
+            _arg(new_lens, _I32, b, "new_lens", dev),
+            _arg(block_table, _I32, (B, mb), "block_table", dev), mb,
+            _arg(free_pages, _I32, (F,), "free_pages", dev), F,
+            _arg(free_count, _I32, one, "free_count", dev), num_pages, T,
+            _arg(query_start, _I32, (B + 1,), "query_start", dev),
+            _arg(positions, _I32, t, "positions", dev), _arg(slots, _I64, t, "slots", dev),
+            None if token_request is None else _arg(token_request, _I32, t, "token_request", dev),
+            _arg(seqlens_out, _I32, b, "seqlens_out", dev),
+            _arg(free_count_out, _I32, one, "free_count_out", dev), ws, nws)
 
 
 def release_pages(seqlens, release, block_table, free_pages, free_count, num_pages, stream=None):
     """mla_release_pages: return the pages of every request with release[b] != 0 to
     the free list (seqlens, block_table, free_pages and free_count in place)."""
-    B = seqlens.shape[0]
-    i32 = torch.int32
-    _need(seqlens, i32, (B,), "seqlens")
-    _need(release, i32, (B,), "release")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_blocks]")
-    _need(block_table, i32, (B, block_table.shape[1]), "block_table")
-    _need(free_pages, i32, (free_pages.numel(),), "free_pages")
-    _need(free_count, i32, (1,), "free_count")
-    dev = _same_device(seqlens, release, block_table, free_pages, free_count)
-    st = _on(dev, stream, load_library().mla_release_pages, B, _ptr(seqlens), _ptr(release),
-             _ptr(block_table), block_table.shape[1], _ptr(free_pages), free_pages.shape[0],
-             _ptr(free_count), num_pages)
-    _check("mla_release_pages", st)
+    dev = _device(seqlens, "seqlens")
+    B, F, mb = seqlens.shape[0], free_pages.numel(), block_table.shape[-1]
+    _launch("mla_release_pages", dev, stream, B, _arg(seqlens, _I32, (B,), "seqlens", dev),
+            _arg(release, _I32, (B,), "release", dev),
+            _arg(block_table, _I32, (B, mb), "block_table", dev), mb,
+            _arg(free_pages, _I32, (F,), "free_pages", dev), F,
+            _arg(free_count, _I32, (1,), "free_count", dev), num_pages)
 
 
 def cache_write_paged(dims: Dims, x, gamma, positions, slots, cache_pool, table=None, eps=1e-6,
@@ -619,28 +645,15 @@ def cache_write_paged(dims: Dims, x, gamma, positions, slots, cache_pool, table=
     """mla_cache_write_paged: the rows [RMSNorm(x_c) * gamma || RoPE(x_r, position)] of
     projected tokens x [T, d_c + d_r] to rows ``slots`` (int64, -1: none) of
     cache_pool [num_pages, 64, d_c + d_r].  Without a table x_r is stored as it is."""
-    dt, T = dims.torch_dtype, x.shape[0]
-    _need_rows(x, dt, dims.R, "x")
-    _need(slots, torch.int64, (T,), "slots")
-    if positions is not None:
-        _need(positions, torch.int32, (T,), "positions")
-    if gamma is not None:
-        _need(gamma, torch.float32, (dims.d_c,), "gamma")
-    _need(cache_pool, dt, (cache_pool.shape[0], PAGE_ROWS, dims.R), "cache_pool")
-    dev = _same_device(x, slots, positions, gamma, cache_pool)
-    st = _on(dev, stream, load_library().mla_cache_write_paged, ctypes.byref(dims.c()), T,
-             x.data_ptr(), x.stride(0) if T > 1 else dims.R, _ptr(gamma), eps, _table_ptr(table),
-             _ptr(positions), _ptr(slots), _ptr(cache_pool), cache_pool.shape[0])
-    _check("mla_cache_write_paged", st)
-
-
-def _need_fp8_pages(dims: Dims, pool, page_scales, block_table):
-    n = pool.shape[0]
-    _need(pool, torch.uint8, (n, PAGE_ROWS, dims.d_c + 2 * dims.d_r), "cache_pool")
-    _need(page_scales, torch.float32, (n,), "page_scales")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_blocks]")
-    _need(block_table, torch.int32, (dims.B, block_table.shape[1]), "block_table")
+    dev = _device(x, "x")
+    dt, R, n = dims.torch_dtype, dims.R, cache_pool.shape[0]
+    px, T, sx = _rows(x, dt, R, dev)
+    _launch("mla_cache_write_paged", dev, stream, dims.ref, T, px, sx,
+            None if gamma is None else _arg(gamma, _F32, (dims.d_c,), "gamma", dev), eps,
+            _table_ptr(table),
+            None if positions is None else _arg(positions, _I32, (T,), "positions", dev),
+            _arg(slots, _I64, (T,), "slots", dev),
+            _arg(cache_pool, dt, (n, PAGE_ROWS, R), "cache_pool", dev), n)
 
 
 def cache_write_fp8_paged(dims: Dims, x, gamma, query_start, seqlens, block_table, cache_pool,
@@ -649,37 +662,33 @@ def cache_write_fp8_paged(dims: Dims, x, gamma, query_start, seqlens, block_tabl
     [num_pages, 64, d_c + 2 d_r] uint8 with one scale per page [num_pages];
     request b's rows are x[query_start[b]:query_start[b+1]], the last of its
     seqlens[b] tokens (the lengths after the step)."""
-    T = x.shape[0]
-    _need_rows(x, dims.torch_dtype, dims.R, "x")
-    _need(query_start, torch.int32, (dims.B + 1,), "query_start")
-    _need(seqlens, torch.int32, (dims.B,), "seqlens")
-    if gamma is not None:
-        _need(gamma, torch.float32, (dims.d_c,), "gamma")
-    _need_fp8_pages(dims, cache_pool, page_scales, block_table)
-    dev = _same_device(x, gamma, query_start, seqlens, block_table, cache_pool, page_scales)
-    st = _on(dev, stream, load_library().mla_cache_write_fp8_paged, ctypes.byref(dims.c()), T,
-             x.data_ptr(), x.stride(0) if T > 1 else dims.R, _ptr(gamma), eps, _table_ptr(table),
-             _ptr(query_start), _ptr(seqlens), _ptr(block_table), block_table.shape[1],
-             _ptr(cache_pool), _ptr(page_scales), cache_pool.shape[0])
-    _check("mla_cache_write_fp8_paged", st)
+    dev = _device(x, "x")
+    B, n, mb = dims.B, cache_pool.shape[0], block_table.shape[-1]
+    px, T, sx = _rows(x, dims.torch_dtype, dims.R, dev)
+    _launch("mla_cache_write_fp8_paged", dev, stream, dims.ref, T, px, sx,
+            None if gamma is None else _arg(gamma, _F32, (dims.d_c,), "gamma", dev), eps,
+            _table_ptr(table), _arg(query_start, _I32, (B + 1,), "query_start", dev),
+            _arg(seqlens, _I32, (B,), "seqlens", dev),
+            _arg(block_table, _I32, (B, mb), "block_table", dev), mb,
+            _arg(cache_pool, torch.uint8, (n, PAGE_ROWS, dims.d_c + 2 * dims.d_r), "cache_pool", dev),
+            _arg(page_scales, _F32, (n,), "page_scales", dev), n)
 
 
 def decode_fp8_paged(dims: Dims, q_cat, cache_pool, page_scales, block_table, seqlens,
                      softmax_scale, workspace, num_splits=0, stream=None) -> int:
     """mla_decode_fp8_paged: mla_decode over an 8-bit paged cache (see
     cache_write_fp8_paged); returns the splits used, for combine."""
-    _need(q_cat, dims.torch_dtype, (dims.B, dims.H, dims.R), "q_cat")
-    _need_fp8_pages(dims, cache_pool, page_scales, block_table)
-    _need(seqlens, torch.int32, (dims.B,), "seqlens")
-    _need_ws(workspace)
+    dev = _device(q_cat, "q_cat")
+    B, n, mb = dims.B, cache_pool.shape[0], block_table.shape[-1]
+    ws, nws = _ws_arg(workspace, dev)
     used = ctypes.c_int(0)
-    dev = _same_device(q_cat, cache_pool, page_scales, block_table, seqlens, workspace)
-    st = _on(dev, stream, load_library().mla_decode_fp8_paged, ctypes.byref(dims.c()),
-             _ptr(q_cat), _ptr(cache_pool), _ptr(page_scales), cache_pool.shape[0],
-             _ptr(block_table), block_table.shape[1], _ptr(seqlens), float(softmax_scale),
-             num_splits, _ptr(workspace), workspace.numel() * workspace.element_size(),
-             ctypes.byref(used))
-    _check("mla_decode_fp8_paged", st)
+    _launch("mla_decode_fp8_paged", dev, stream, dims.ref,
+            _arg(q_cat, dims.torch_dtype, (B, dims.H, dims.R), "q_cat", dev),
+            _arg(cache_pool, torch.uint8, (n, PAGE_ROWS, dims.d_c + 2 * dims.d_r), "cache_pool", dev),
+            _arg(page_scales, _F32, (n,), "page_scales", dev), n,
+            _arg(block_table, _I32, (B, mb), "block_table", dev), mb,
+            _arg(seqlens, _I32, (B,), "seqlens", dev), float(softmax_scale), num_splits, ws, nws,
+            ctypes.byref(used))
     return used.value
 
 

@@ -83,7 +83,13 @@ cache_write_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
     const int c = (lane + 32 * u) * kVec;
     v[u] = c < d_c ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
   }
+  // Everything else that is read is asked for before the first use of x.
   const int64_t slot = slots[t];
+  const int64_t pos = rotate ? positions[t] : 0;
+  int pi = lane, pj = lane + d_r / 2;
+  if (rotate) pair_at(tab, d_r, lane, &pi, &pj);
+  float pa = 0.f, pb = 0.f;
+  if (lane < d_r / 2) pa = Storage<T>::to_f(row[d_c + pi]), pb = Storage<T>::to_f(row[d_c + pj]);
   if (slot < 0) return;               // padding
   if (slot >= total_rows) {
     if (lane == 0) record_status(status, MLA_ERR_BOUNDS);
@@ -97,7 +103,7 @@ cache_write_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
 #pragma unroll
     for (int i = 0; i < kVec; ++i) ss = fmaf(f[i], f[i], ss);
   }
-  const float inv = 1.f / sqrtf(warp_sum(ss) / float(d_c) + eps);
+  const float inv = rsqrtf(warp_sum(ss) / float(d_c) + eps);
   T* dst = pool + slot * (d_c + d_r);
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
@@ -111,30 +117,36 @@ cache_write_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
       *reinterpret_cast<uint4*>(dst + c) = pack16<T, kVec>(f);
     }
   }
-  const int64_t pos = rotate ? positions[t] : 0;
-  for (int k = lane; k < d_r / 2; k += 32) {
-    int i = k, j = k + d_r / 2;
-    float c = 1.f, s = 0.f;
-    if (rotate) {
-      pair_at(tab, d_r, k, &i, &j);
-      rope_turn_cos_sin(tab.turn[k], pos, tab.amplitude, &c, &s);
+  for (int k = lane; k < d_r / 2; k += 32) {   // one pair per lane up to d_r = 64
+    if (k != lane) {
+      pi = k, pj = k + d_r / 2;
+      if (rotate) pair_at(tab, d_r, k, &pi, &pj);
+      pa = Storage<T>::to_f(row[d_c + pi]), pb = Storage<T>::to_f(row[d_c + pj]);
     }
-    const float a = Storage<T>::to_f(row[d_c + i]), b = Storage<T>::to_f(row[d_c + j]);
-    dst[d_c + i] = Storage<T>::from_f(rotate ? a * c - b * s : a);
-    dst[d_c + j] = Storage<T>::from_f(rotate ? a * s + b * c : b);
+    if (rotate) {
+      float c, s;
+      rope_turn_cos_sin(tab.turn[k], pos, tab.amplitude, &c, &s);
+      const float a = pa, b = pb;
+      pa = a * c - b * s;
+      pb = a * s + b * c;
+    }
+    dst[d_c + pi] = Storage<T>::from_f(pa);
+    dst[d_c + pj] = Storage<T>::from_f(pb);
   }
 }
 
 // ---------------------------------------------------------------- 8-bit pages
 // One block per (request, page that its new tokens touch), at most 64 rows.
-// Each warp keeps its rows in registers (one read of x), the page's largest
-// magnitude is reduced over the block, the new exponent fixed, and the codes
-// written.  If the page held rows before and its scale grows, those rows are
-// rescaled first by a power of two, which is exact for the rotary keys and for
-// codes that stay normal E4M3 values and rounds the others once more.
+// Bound by latency (a decode step; a page per SM for prompts of some thousand
+// tokens).  The rows are copied to shared memory asynchronously (one read of x,
+// all in flight at once; two blocks share an SM: held in registers, a block
+// filled it and 150 pages took two waves), each warp norms its own, the page's
+// largest magnitude is reduced over the block, the new exponent fixed, and the
+// codes written.  If the page held rows before and its scale grows, those rows
+// are rescaled first by a power of two, which is exact for the rotary keys and
+// for codes that stay normal E4M3 values and rounds the others once more.
 constexpr int k8Threads = 512;
 constexpr int k8Warps = k8Threads / 32;
-constexpr int k8Rows = kTileKeys / k8Warps;   // rows per warp
 constexpr int k8Dc = 512;
 constexpr int kMinScaleExp = -40, kMaxScaleExp = 120;
 
@@ -160,7 +172,7 @@ __device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float f) {
 }
 
 template <int kDr>
-__global__ void __launch_bounds__(k8Threads)
+__global__ void __launch_bounds__(k8Threads, 2)
 cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
                     const __nv_bfloat16* __restrict__ x, int64_t x_stride, int T_rows,
                     const float* __restrict__ gamma, float eps,
@@ -168,9 +180,10 @@ cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
                     int B, int64_t cap, const PageMap pm, uint8_t* __restrict__ pool,
                     float* __restrict__ page_scales, int* __restrict__ status) {
   constexpr int kRowBytes = k8Dc + 2 * kDr;
+  extern __shared__ __align__(16) uint8_t s_x[];   // [64 rows][d_c + d_r] bf16 as they came
   __shared__ int s_scan[k8Warps];
   __shared__ int s_req, s_first, s_total;
-  __shared__ float s_max[k8Warps];
+  __shared__ float s_max[k8Warps], s_inv[kTileKeys];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
 
@@ -215,55 +228,58 @@ cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
   const int64_t q0 = query_start[b], end = seqlens[b];
   const int64_t start = end - (query_start[b + 1] - q0);        // first new position
   const int64_t j = start / kTileKeys + (task - s_first);       // this page's block
-  const int64_t first = pm.tile_row(b, j);
-  if (first < 0) {
-    if (tid == 0) record_status(status, MLA_ERR_BOUNDS);
-    return;
-  }
   const int r0 = int(max(start - j * kTileKeys, int64_t(0)));                    // new rows
   const int r1 = int(min(end - j * kTileKeys, int64_t(kTileKeys)));              // [r0, r1)
   const int64_t x0 = q0 + j * kTileKeys - start;                                 // x row of page row 0
-  uint8_t* page = pool + first * kRowBytes;
-  float* page_scale = page_scales + first / kTileKeys;
-  const float old_scale = r0 ? *page_scale : 0.f;
+  // The page id and x are asked for together.
+  const int64_t first = pm.tile_row(b, j);
 
-  // Rows r0 + warp, r0 + warp + 16, ... of the page: 16 values of each per lane.
-  uint4 v[k8Rows][2];
-  float p1[k8Rows], p2[k8Rows];
+  // Rows r0 + warp, r0 + warp + 16, ... of the page are this warp's.
+  constexpr int kXBytes = 2 * (k8Dc + kDr);
+#pragma unroll 1
+  for (int r = r0 + warp; r < r1; r += k8Warps) {
+    const char* src = reinterpret_cast<const char*>(x + (x0 + r) * x_stride);
+    const uint32_t dst = uint32_t(__cvta_generic_to_shared(s_x + r * kXBytes));
 #pragma unroll
-  for (int i = 0; i < k8Rows; ++i) {
-    const int r = r0 + warp + i * k8Warps;
-    if (r < r1) {
-      const __nv_bfloat16* row = x + (x0 + r) * x_stride;
-      v[i][0] = reinterpret_cast<const uint4*>(row)[lane];
-      v[i][1] = reinterpret_cast<const uint4*>(row)[lane + 32];
-      if constexpr (kDr > 0) {
-        int a = lane, c = lane + kDr / 2;
-        if (rotate) pair_at(tab, kDr, lane, &a, &c);
-        p1[i] = __bfloat162float(row[k8Dc + a]);
-        p2[i] = __bfloat162float(row[k8Dc + c]);
-      }
-    } else {
-      v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
-      p1[i] = p2[i] = 0.f;
-    }
+    for (int u = lane; u < kXBytes / 16; u += 32)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + u * 16), "l"(src + u * 16)
+                   : "memory");
   }
   float g[16];
   load_gamma(gamma, lane * 8, 8, g);
   load_gamma(gamma, 256 + lane * 8, 8, g + 8);
-  float inv[k8Rows], amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < k8Rows; ++i) {
+  if (first < 0) {
+    if (tid == 0) record_status(status, MLA_ERR_BOUNDS);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
+  uint8_t* page = pool + first * kRowBytes;
+  float* page_scale = page_scales + first / kTileKeys;
+  const float old_scale = r0 ? *page_scale : 0.f;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  auto row_values = [&](int r, float (&f)[16]) {
+    const uint4* row = reinterpret_cast<const uint4*>(s_x + r * kXBytes);
+    unpack16<__nv_bfloat16, 8>(row[lane], *reinterpret_cast<float(*)[8]>(f));
+    unpack16<__nv_bfloat16, 8>(row[lane + 32], *reinterpret_cast<float(*)[8]>(f + 8));
+  };
+  // This lane's pair (read once: lanes differ, so the table read is serialised).
+  int ra = lane, rc = lane + kDr / 2;
+  const uint64_t turn = kDr > 0 && rotate ? tab.turn[lane] : 0;
+  if (kDr > 0 && rotate) pair_at(tab, kDr, lane, &ra, &rc);
+  // The loops over a warp's rows stay rolled: a page is written once, so what
+  // its code costs is mostly the fetching of it.
+  float amax = 0.f;
+#pragma unroll 1
+  for (int r = r0 + warp; r < r1; r += k8Warps) {
     float f[16], ss = 0.f;
-    unpack16<__nv_bfloat16, 8>(v[i][0], *reinterpret_cast<float(*)[8]>(f));
-    unpack16<__nv_bfloat16, 8>(v[i][1], *reinterpret_cast<float(*)[8]>(f + 8));
+    row_values(r, f);
 #pragma unroll
     for (int e = 0; e < 16; ++e) ss = fmaf(f[e], f[e], ss);
-    inv[i] = 1.f / sqrtf(warp_sum(ss) / float(k8Dc) + eps);
-    if (r0 + warp + i * k8Warps < r1) {
+    const float inv = rsqrtf(warp_sum(ss) * (1.f / k8Dc) + eps);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(f[e] * inv[i] * g[e]));
-    }
+    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(f[e] * inv * g[e]));
+    if (lane == 0) s_inv[r] = inv;
   }
   amax = warp_max(amax);
   if (lane == 0) s_max[warp] = amax;
@@ -296,34 +312,32 @@ cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
   }
   const float inv_scale = ldexpf(1.f, -k);
   if (tid == 0) *page_scale = ldexpf(1.f, k);
-#pragma unroll
-  for (int i = 0; i < k8Rows; ++i) {
-    const int r = r0 + warp + i * k8Warps;
-    if (r >= r1) continue;
+#pragma unroll 1
+  for (int r = r0 + warp; r < r1; r += k8Warps) {
+    const float inv = s_inv[r] * inv_scale;   // the power of two commutes with the roundings
     uint8_t* row = page + r * kRowBytes;
     float f[16];
-    unpack16<__nv_bfloat16, 8>(v[i][0], *reinterpret_cast<float(*)[8]>(f));
-    unpack16<__nv_bfloat16, 8>(v[i][1], *reinterpret_cast<float(*)[8]>(f + 8));
+    row_values(r, f);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) f[e] = f[e] * inv[i] * g[e] * inv_scale;
+    for (int e = 0; e < 16; ++e) f[e] = f[e] * inv * g[e];
     reinterpret_cast<uint2*>(row)[lane] =
         make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
     reinterpret_cast<uint2*>(row)[lane + 32] =
         make_uint2(e4m3x4(f[8], f[9], f[10], f[11]), e4m3x4(f[12], f[13], f[14], f[15]));
     if constexpr (kDr > 0) {
-      int a = lane, c = lane + kDr / 2;
-      float y1 = p1[i], y2 = p2[i];
+      const __nv_bfloat16* xr = reinterpret_cast<const __nv_bfloat16*>(s_x + r * kXBytes) + k8Dc;
+      const float a = __bfloat162float(xr[ra]), c = __bfloat162float(xr[rc]);
+      float y1 = a, y2 = c;
       if (rotate) {
-        pair_at(tab, kDr, lane, &a, &c);
         float cs, sn;
-        rope_turn_cos_sin(tab.turn[lane], j * kTileKeys + r, tab.amplitude, &cs, &sn);
-        y1 = p1[i] * cs - p2[i] * sn;
-        y2 = p1[i] * sn + p2[i] * cs;
+        rope_turn_cos_sin(turn, j * kTileKeys + r, tab.amplitude, &cs, &sn);
+        y1 = a * cs - c * sn;
+        y2 = a * sn + c * cs;
       }
       // Rounded to bf16 as in a bf16 cache; the power of two is exact.
       __nv_bfloat16* rope = reinterpret_cast<__nv_bfloat16*>(row + k8Dc);
-      rope[a] = __float2bfloat16_rn(__bfloat162float(__float2bfloat16_rn(y1)) * inv_scale);
-      rope[c] = __float2bfloat16_rn(__bfloat162float(__float2bfloat16_rn(y2)) * inv_scale);
+      rope[ra] = __float2bfloat16_rn(__bfloat162float(__float2bfloat16_rn(y1)) * inv_scale);
+      rope[rc] = __float2bfloat16_rn(__bfloat162float(__float2bfloat16_rn(y2)) * inv_scale);
     }
   }
 }
@@ -368,7 +382,11 @@ cudaError_t launch_cache_write_fp8(const mla_rope_table* tab, const __nv_bfloat1
   const int64_t most = int64_t(T_rows) / kTileKeys + 2 * int64_t(B);
   const dim3 grid(unsigned(most < T_rows ? most : T_rows));
   auto kernel = d_r ? cache_write8_kernel<64> : cache_write8_kernel<0>;
-  return launch_pdl(kernel, grid, dim3(k8Threads), 0, stream, t, int(tab != nullptr), x, x_stride,
+  const size_t smem = size_t(kTileKeys) * 2 * (k8Dc + d_r);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             int(smem));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, grid, dim3(k8Threads), smem, stream, t, int(tab != nullptr), x, x_stride,
                     T_rows, gamma, eps, query_start, seqlens, B, cap, pm, pool, page_scales,
                     status);
 }

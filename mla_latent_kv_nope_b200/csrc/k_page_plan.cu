@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     if (blockIdx.x == 0 && b < a.B) a.query_start[b + 1] = te;
     __syncthreads();
     const int32_t tok_end = s_tok[kPlanThreads - 1], page_end = s_page[kPlanThreads - 1];
+#pragma unroll 4
     for (int32_t t = max(t0, tok_base) + tid; t < min(live1, tok_end); t += kPlanThreads) {
       const int r = first_past(s_tok, kPlanThreads, t);
       const int64_t Lr = s_len[r], have = pages_of(Lr);
