@@ -61,10 +61,10 @@ template <> struct RopeVec<float> {
   }
 };
 
-// Block = `toks` tokens x `heads` heads, one thread per 8 pairs of a row
-// (toks * heads * (d_r / 16) <= kRopeThreads).  d_r % 16 == 0, 16-byte aligned
-// rows.
-template <typename T>
+// Block = `toks` tokens x kBlocks * `heads` heads, one thread per 8 pairs of
+// kBlocks rows (toks * heads * (d_r / 16) <= kRopeThreads).  d_r % 16 == 0,
+// 16-byte aligned rows.
+template <typename T, int kBlocks>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_vec_kernel(const __grid_constant__ mla_rope_table tab, const T* __restrict__ x, int64_t xt,
                 int64_t xh, const int32_t* __restrict__ pos, T* y, int64_t yt, int64_t yh,
@@ -75,16 +75,20 @@ rope_vec_kernel(const __grid_constant__ mla_rope_table tab, const T* __restrict_
   const int row = threadIdx.x / tpr, g = threadIdx.x % tpr;
   const int tl = row / heads;
   const int64_t tok = tok0 + tl;
-  const int head = blockIdx.y * heads + row % heads;
-  const bool live = tl < toks && tok < n_tokens && head < H;
+  const int head0 = blockIdx.y * kBlocks * heads + row % heads;
+  const bool live = tl < toks && tok < n_tokens;
   const bool inter = tab.layout == MLA_ROPE_INTERLEAVED;
   const int o1 = inter ? 16 * g : 8 * g, o2 = inter ? 16 * g + 8 : half + 8 * g;
   pdl_wait();
-  RopeVec<T> v1, v2;
-  if (live) {
-    const T* p = x + tok * xt + head * xh;
-    v1.load(p + o1);
-    v2.load(p + o2);
+  RopeVec<T> v1[kBlocks], v2[kBlocks];
+#pragma unroll
+  for (int k = 0; k < kBlocks; ++k) {
+    const int head = head0 + k * heads;
+    if (live && head < H) {
+      const T* p = x + tok * xt + head * xh;
+      v1[k].load(p + o1);
+      v2[k].load(p + o2);
+    }
   }
   for (int i = threadIdx.x; i < toks * half; i += kRopeThreads) {
     const int64_t t = tok0 + i / half;
@@ -97,34 +101,39 @@ rope_vec_kernel(const __grid_constant__ mla_rope_table tab, const T* __restrict_
   }
   __syncthreads();
   if (!live) return;
-  float a[8], b[8];
-  v1.get(a);
-  v2.get(b);
   const float2* cs = s_cs + tl * half + 8 * g;
-  if (inter) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 c0 = cs[i], c1 = cs[4 + i];
-      const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
-      a[2 * i] = a0 * c0.x - a1 * c0.y;
-      a[2 * i + 1] = a0 * c0.y + a1 * c0.x;
-      b[2 * i] = b0 * c1.x - b1 * c1.y;
-      b[2 * i + 1] = b0 * c1.y + b1 * c1.x;
-    }
-  } else {
+  for (int k = 0; k < kBlocks; ++k) {
+    const int head = head0 + k * heads;
+    if (head >= H) break;
+    float a[8], b[8];
+    v1[k].get(a);
+    v2[k].get(b);
+    if (inter) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 c = cs[i];
-      const float x1 = a[i], x2 = b[i];
-      a[i] = x1 * c.x - x2 * c.y;
-      b[i] = x1 * c.y + x2 * c.x;
+      for (int i = 0; i < 4; ++i) {
+        const float2 c0 = cs[i], c1 = cs[4 + i];
+        const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
+        a[2 * i] = a0 * c0.x - a1 * c0.y;
+        a[2 * i + 1] = a0 * c0.y + a1 * c0.x;
+        b[2 * i] = b0 * c1.x - b1 * c1.y;
+        b[2 * i + 1] = b0 * c1.y + b1 * c1.x;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 c = cs[i];
+        const float x1 = a[i], x2 = b[i];
+        a[i] = x1 * c.x - x2 * c.y;
+        b[i] = x1 * c.y + x2 * c.x;
+      }
     }
+    v1[k].set(a);
+    v2[k].set(b);
+    T* q = y + tok * yt + head * yh;
+    v1[k].store(q + o1);
+    v2[k].store(q + o2);
   }
-  v1.set(a);
-  v2.set(b);
-  T* q = y + tok * yt + head * yh;
-  v1.store(q + o1);
-  v2.store(q + o2);
 }
 
 // Any even d_r and any strides: one thread per pair.
@@ -170,9 +179,14 @@ cudaError_t launch_rope(const mla_rope_table& tab, int64_t n_tokens, int H, cons
     const int rows = kRopeThreads / (tab.d_r / 16);
     const int heads = H < rows ? H : rows;
     const int toks = rows / heads;
-    const dim3 grid(unsigned((n_tokens + toks - 1) / toks), unsigned((H + heads - 1) / heads));
-    return launch_pdl(rope_vec_kernel<T>, grid, dim3(kRopeThreads), 0, stream, tab, x, xt, xh, pos,
-                      y, yt, yh, n_tokens, H, toks, heads, transpose);
+    // Two rows a thread where a token has that many heads: twice the loads in
+    // flight and half the angles.
+    const int blocks = sizeof(T) == 2 && H >= 2 * heads ? 2 : 1;
+    const dim3 grid(unsigned((n_tokens + toks - 1) / toks),
+                    unsigned((H + blocks * heads - 1) / (blocks * heads)));
+    return launch_pdl(blocks == 2 ? rope_vec_kernel<T, 2> : rope_vec_kernel<T, 1>, grid,
+                      dim3(kRopeThreads), 0, stream, tab, x, xt, xh, pos, y, yt, yh, n_tokens, H,
+                      toks, heads, transpose);
   }
   const int64_t n = n_tokens * H * (tab.d_r / 2);
   const int64_t blocks = (n + kRopeThreads - 1) / kRopeThreads;
