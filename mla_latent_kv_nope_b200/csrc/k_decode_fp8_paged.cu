@@ -55,23 +55,14 @@
 // Every wait is bounded (about 2 s of SM cycles); on give-up a CTA raises the
 // abort flag of both, records MLA_ERR_DEVICE_TIMEOUT, drains its own loads and
 // products and exits.
-#include <cuda.h>
-#include <cuda_fp8.h>
-
-#include "common.cuh"
-#include "kernels.h"
-#include "sm100.cuh"
-#include "tensor_map.cuh"
+#include "decode8.cuh"
 
 namespace mla {
 
 namespace {
 
-using namespace sm100;
+using namespace decode8;
 
-constexpr int kHeadsPerCta = 64;
-constexpr int kDc = 512;
-constexpr int kChunk = 8192;              // 64 rows x 128 bytes, 128-byte swizzle
 constexpr int kKStages = 2, kVStages = 3;   // V: and P, page by page
 constexpr int kKBytes = 5 * kChunk;       // 4 chunks of codes, 1 of RoPE keys
 constexpr int kVBytes = 2 * kChunk;
@@ -82,17 +73,10 @@ constexpr int kKWarp = kSoftmaxWarps, kQkWarp = kKWarp + 1, kVWarp = kKWarp + 2,
 constexpr int kThreads = kSoftmaxThreads + 4 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256;    // O: 2 x 128 columns, S: 2 x 64
-constexpr float kPScale = 6.75f;          // probabilities are held times 2^6.75
-constexpr float kRise = 2.f, kFall = 13.f;   // log2; 2^(6.75 + 2) = 430.5 <= 448
-// Where a reference starts above the maximum of the tile that moves it: the
-// first one, a higher one (the next are likely lower) and a lower one.
-constexpr float kLeadFirst = 8.f, kLeadUp = 6.f, kLeadDown = 9.f;
-constexpr float kTopWindow = 60.f;
 
 constexpr uint32_t kIdescQK = idesc_f16_f32(128, 128, false, false);   // E4M3 is format 0 too
 constexpr uint32_t kIdescRope = idesc_bf16_f32(128, 128, false, false);
 constexpr uint32_t kIdescPV = idesc_f16_f32(128, 256, false, true);
-constexpr uint32_t kE5m2A = 1u << 7;      // A's format field: E5M2 (lo) instead of E4M3 (hi)
 
 struct Bars {
   uint64_t kfull[kKStages];   // leader's: both CTAs' stages have landed
@@ -119,161 +103,6 @@ __device__ __forceinline__ void raise_abort(Bars* bars, int* status) {
   record_status(status, MLA_ERR_DEVICE_TIMEOUT);
 }
 
-// Warp-uniform bounded wait (all lanes poll; lane 0 owns the limit).
-__device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                       uint64_t limit = kWaitLimitCycles) {
-  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-  const uint64_t t0 = sm_cycles();
-  for (;;) {
-    if (__all_sync(0xffffffffu, mbar_try_for(bar, parity, 20000))) return true;
-    {
-      int give_up = 0;
-      if ((threadIdx.x & 31) == 0) give_up = (*abort_flag != 0) || (sm_cycles() - t0 > limit);
-      if (__shfl_sync(0xffffffffu, give_up, 0)) return false;
-    }
-  }
-}
-
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
-  const __half2 h(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(c), __NV_E4M3));
-  return __half22float2(h);
-}
-
-// The sequences whose tiles lie in this worker's range of work units (as in
-// tile_deal.cuh, for any batch size): every role walks them by itself from the
-// first one, whose number and unit prefix the block finds together.
-struct Segments {
-  const int32_t* seqlens;
-  int B, b;             // b: the sequence after the current one
-  int64_t cap, pre, u0, u1;
-  int32_t len_b;        // its length, read ahead
-  int cur;              // the current sequence, its tiles [lo, hi) and length
-  int64_t lo, hi, L;
-  __device__ bool next() {
-    while (b < B && pre < u1) {
-      cur = b++;
-      L = clamp_len(len_b, cap);
-      if (b < B) len_b = seqlens[b];
-      const int64_t nt = tiles_of(L), r0 = pre + kSwitchUnits;
-      if (nt == 0) continue;
-      pre = r0 + nt;
-      lo = max(r0, u0) - r0;
-      hi = min(r0 + nt, u1) - r0;
-      if (lo < hi) return true;
-    }
-    return false;
-  }
-};
-
-// All threads; `scratch` is shared memory for kThreads / 32 + 3 values.  False
-// if the worker has no units.
-__device__ __forceinline__ bool find_segments(const int32_t* seqlens, int B, int64_t cap, int w,
-                                              int W, int64_t* scratch, Segments* out) {
-  constexpr int kWarps = kThreads / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t len0 = int(threadIdx.x) < B ? seqlens[threadIdx.x] : 0;
-  int64_t sum = units_of(clamp_len(len0, cap));
-  for (int b = threadIdx.x + kThreads; b < B; b += kThreads)
-    sum += units_of(clamp_len(seqlens[b], cap));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) scratch[warp] = sum;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int k = 0; k < kWarps; ++k) total += scratch[k];
-  __syncthreads();
-  const int64_t u0 = worker_tile_begin(w, total, W), u1 = worker_tile_begin(w + 1, total, W);
-  if (u0 >= u1) return false;
-  // The sequence that unit u0 belongs to, kThreads of them at a time.
-  int64_t base = 0;
-#pragma unroll 1
-  for (int b0 = 0;; b0 += kThreads) {
-    const int b = b0 + int(threadIdx.x);
-    const int32_t len = b0 == 0 ? len0 : b < B ? seqlens[b] : 0;
-    const int64_t n = b < B ? units_of(clamp_len(len, cap)) : 0;
-    int64_t e = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, e, o);
-      if (lane >= o) e += u;
-    }
-    if (lane == 31) scratch[warp] = e;
-    __syncthreads();
-    int64_t chunk = 0;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      if (k < warp) e += scratch[k];
-      chunk += scratch[k];
-    }
-    e += base;
-    if (u0 < e && u0 >= e - n)
-      scratch[kWarps] = b, scratch[kWarps + 1] = e - n, scratch[kWarps + 2] = len;
-    __syncthreads();
-    base += chunk;
-    if (u0 < base) break;      // u0 < total, so some chunk holds it
-  }
-  *out = Segments{seqlens, B,  int(scratch[kWarps]),         cap, scratch[kWarps + 1],
-                  u0,      u1, int32_t(scratch[kWarps + 2]), 0,   0,
-                  0,       0};
-  __syncthreads();             // before the scratch is used for anything else
-  return true;
-}
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
-      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
-// Page rows and scales of a run of tiles: lane l holds tile base + l, and the
-// 32 after those are already on their way.
-struct PageWalk {
-  const PageMap& pm;
-  const float* scales;   // or null
-  int b, lane;
-  int64_t base, hi;
-  int64_t row, row_next;
-  float sc, sc_next;
-  __device__ PageWalk(const PageMap& m, const float* s, int b_, int64_t lo, int64_t hi_)
-      : pm(m), scales(s), b(b_), lane(threadIdx.x & 31), base(lo), hi(hi_) {
-    fetch(lo, row, sc);
-    fetch(lo + 32, row_next, sc_next);
-  }
-  __device__ void fetch(int64_t t0, int64_t& r, float& s) const {
-    const int64_t t = t0 + lane;
-    r = t < hi ? pm.tile_row(b, t) : -1;
-    s = scales && r >= 0 ? scales[r / kTileKeys] : 1.f;
-  }
-  // Row (-1: outside the pool) and scale of tile t >= base, the same in all lanes.
-  __device__ void at(int64_t t, int64_t* r, float* s) {
-    if (t >= base + 32) {
-      base += 32;
-      row = row_next, sc = sc_next;
-      fetch(base + 32, row_next, sc_next);
-    }
-    *r = __shfl_sync(0xffffffffu, row, int(t - base));
-    *s = __shfl_sync(0xffffffffu, sc, int(t - base));
-  }
-};
-
 template <int kDr>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
@@ -291,6 +120,9 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
   const int g = blockIdx.x, w = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  pdl_wait();
+  // Asked for before the setup that it does not depend on.
+  const int32_t len0 = int(threadIdx.x) < B ? seqlens[threadIdx.x] : 0;
   if (threadIdx.x == 0) {
     // The leader's also wait for the other CTA's word that its stage has landed.
     const uint32_t n_full = rank == 0 ? 2 : 1;
@@ -326,9 +158,9 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
   const uint32_t tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort_flag;
 
-  pdl_wait();     // everything above is independent of what earlier kernels write
   Segments seg;
-  const bool busy = find_segments(seqlens, B, cap, w, W, reinterpret_cast<int64_t*>(smem), &seg);
+  const bool busy = find_segments<kThreads>(len0, seqlens, B, cap, w, W,
+                                            reinterpret_cast<int64_t*>(smem), &seg);
   uint32_t n_issued = 0;     // K or V stages that this producer warp has loaded into
   bool ok = true;
 
@@ -554,12 +386,9 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           top[r] = __reduce_max_sync(0xffffffffu, top[r]);
-          // Smallest k with top <= 448 * 2^k = 1.75 * 2^(8 + k), kept where 2^k and
-          // 2^-k are normal: top = m 2^(e - 127), 7 mantissa bits, m <= 1.75 up to 96 / 128.
-          const int k =
-              min(max(int(top[r] >> 7) - 127 - 8 + ((top[r] & 0x7Fu) > 96u), -120), 120);
-          inv[r] = __uint_as_float(uint32_t(127 - k) << 23);
-          if (lane == 0) s_row[8 * warp + r0 + r] = __uint_as_float(uint32_t(127 + k) << 23);
+          const int k = query_exponent(top[r]);
+          inv[r] = exp2i(-k);
+          if (lane == 0) s_row[8 * warp + r0 + r] = exp2i(k);
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -568,13 +397,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
           for (int e = 0; e < 2; ++e) {
             uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float a = __uint_as_float(wd[r][4 * e + x] << 16) * inv[r];
-              const float c = __uint_as_float(wd[r][4 * e + x] & 0xFFFF0000u) * inv[r];
-              hi[x] = e4m3x2(a, c);
-              const float2 back = from_e4m3x2(hi[x]);
-              lo[x] = e4m3x2(a - back.x, c - back.y);
-            }
+            for (int x = 0; x < 4; ++x) split_query(wd[r][4 * e + x], inv[r], &hi[x], &lo[x]);
             const int un = lane + 32 * e;    // 8 codes: half of 16-byte unit (un % 16) / 2
             const int off = (un / 16) * kChunk + qr * 128 + ((((un % 16) >> 1) ^ (qr & 7)) * 16) +
                             (un & 1) * 8;
@@ -586,12 +409,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
           if (kDr && lane < kDr / 8) {
             uint32_t o[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const __nv_bfloat162 p =
-                  __floats2bfloat162_rn(__uint_as_float(rd[r][x] << 16) * inv[r],
-                                        __uint_as_float(rd[r][x] & 0xFFFF0000u) * inv[r]);
-              o[x] = *reinterpret_cast<const uint32_t*>(&p);
-            }
+            for (int x = 0; x < 4; ++x) o[x] = scale_bf16x2(rd[r][x], inv[r]);
             *reinterpret_cast<uint4*>(smem + kOffQ + 8 * kChunk + qr * 128 +
                                       ((lane ^ (qr & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
@@ -655,38 +473,16 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
           ref = mt + kLeadFirst;
         } else {
           top = fmaxf(top, mt);
-          const float to = fmaxf(mt, top - kTopWindow);
-          const bool up = to > ref + kRise;
-          if (up || to < ref - kFall) {
-            const float next = to + (up ? kLeadUp : kLeadDown);
+          const float next = next_reference(ref, mt, top);
+          if (next != ref) {
             alpha = ex2_approx(ref - next);
             ref = next;
             l_sum *= alpha;
           }
         }
         const float shift = lsc + kPScale - ref;
-        // p = 2^(s f + shift), as hi (E4M3) + lo (E5M2), through fp16.
-        float2 sum2 = make_float2(0.f, 0.f);
         uint32_t hi8[8], lo8[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint32_t h[2], l[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float2 z = fma2(make_float2(__uint_as_float(x[4 * j + 2 * e]),
-                                              __uint_as_float(x[4 * j + 2 * e + 1])),
-                                  make_float2(f, f), make_float2(shift, shift));
-            const float2 p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
-            sum2 = add2(sum2, p);
-            const __half2 p16 = __floats2half2_rn(p.x, p.y);
-            h[e] = __nv_cvt_halfraw2_to_fp8x2(p16, __NV_SATFINITE, __NV_E4M3);
-            const __half2 back(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(h[e]), __NV_E4M3));
-            l[e] = __nv_cvt_halfraw2_to_fp8x2(__hsub2(p16, back), __NV_SATFINITE, __NV_E5M2);
-          }
-          hi8[j] = h[0] | (h[1] << 16);
-          lo8[j] = l[0] | (l[1] << 16);
-        }
-        const float sum = sum2.x + sum2.y;
+        const float sum = split_probabilities(x, f, shift, hi8, lo8);
         l_sum = fmaf(sum, 1.f / sc, l_sum);
 
         if (t != lo && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -710,7 +506,13 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
         // once the product that read it last is done.
         const uint32_t vp = v + uint32_t(pg);
         const int ps = vp % kVStages;
-        if (t + pg < hi && vp >= kVStages) await(&bars->vempty[ps], (vp / kVStages - 1) & 1);
+        // Without one, the tile before last must be through: this warp's word for
+        // this tile must not count for that one while the other CTA's is on its way.
+        if (t + pg < hi) {
+          if (vp >= kVStages) await(&bars->vempty[ps], (vp / kVStages - 1) & 1);
+        } else if (i >= 2) {
+          await(&bars->pv_done[sb], ((i >> 1) - 1) & 1);
+        }
         if (t + pg < hi) {
           uint8_t* prow = smem + kOffP + ps * kChunk + row * 128;
 #pragma unroll
@@ -806,20 +608,6 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
   }
 }
 
-// Byte map over the rows of the pool: boxes of 128 codes x 64 rows, 128-byte
-// swizzled; rows past the end read as zeros.
-bool make_code_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes) {
-  EncodeTiledFnT fn = encode_tiled_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {row_bytes, rows};
-  const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {128, cuuint32_t(kTileKeys)};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int kDr, typename... Args>
 cudaError_t launch_t(dim3 grid, cudaStream_t stream, Args... args) {
   static bool attr_done[64] = {false};
@@ -839,7 +627,16 @@ inline int head_pairs(int H) { return (H + 2 * kHeadsPerCta - 1) / (2 * kHeadsPe
 
 }  // namespace
 
+// The kernel for up to 64 heads (k_decode_fp8_paged64.cu).
+cudaError_t launch_decode_fp8_paged64(const CUtensorMap& tm_codes, const CUtensorMap& tm_rope,
+                                      const __nv_bfloat16* q_cat, const float* page_scales,
+                                      const PageMap& pm, const int32_t* seqlens, int B, int H,
+                                      int d_r, int64_t cap, float scale_log2, int W, float* o_part,
+                                      float* lse_part, int* status, uint64_t inject_wait,
+                                      cudaStream_t stream);
+
 int decode_fp8_paged_splits(int sms, int H) {
+  if (H <= kHeadsPerCta) return sms;
   const int W = sms / (2 * head_pairs(H));
   return W < 1 ? 1 : W;
 }
@@ -856,8 +653,12 @@ cudaError_t launch_decode_fp8_paged(const __nv_bfloat16* q_cat, const uint8_t* p
   // The same rows viewed as bf16: the RoPE keys are columns 256 .. 319.
   if (d_r && !make_map16(&tm_rope, pool, rows, row_bytes / 2, row_bytes / 2, kTileKeys))
     return cudaErrorInvalidValue;
-  const dim3 grid(2 * head_pairs(H), W);
   const float scale_log2 = scale * 1.4426950408889634f;
+  if (H <= kHeadsPerCta)   // a pair's second CTA would have no heads
+    return launch_decode_fp8_paged64(tm_codes, tm_rope, q_cat, page_scales, pm, seqlens, B, H, d_r,
+                                     cap, scale_log2, W, o_part, lse_part, status, inject_wait,
+                                     stream);
+  const dim3 grid(2 * head_pairs(H), W);
   auto launch = d_r ? launch_t<64, CUtensorMap, CUtensorMap, const float*, PageMap,
                                const __nv_bfloat16*, const int32_t*, int, int, int64_t, float, int,
                                float*, float*, int*, uint64_t>
