@@ -444,9 +444,10 @@ MLA_API int mla_cache_write_paged(const mla_dims* dims, int32_t T, const void* x
  * merges); its default split count never exceeds mla_decode_default_splits.
  * Shape of both: bf16, d_c = 512, d_r = 64 or 0.  page_scales of pages that are read must
  * be positive powers of two (as the write leaves them).  Precision: each query
- * row and the probabilities enter the 8-bit products as sums of two E4M3 terms
- * (the query exact to 2^-18 of its row's largest value, probabilities to 2^-8),
- * with fp32 sums; queries must be finite. */
+ * row and the probabilities enter the 8-bit products as sums of two 8-bit terms
+ * (the query as E4M3 + E4M3, exact to 2^-18 of its row's largest value; a
+ * probability as E4M3 + E5M2, 2^-7 of itself at most and a few times less on
+ * average), with fp32 sums; queries must be finite. */
 MLA_API int mla_cache_write_fp8_paged(const mla_dims* dims, int32_t T, const void* x,
                                       int64_t x_stride, const float* gamma, float eps,
                                       const mla_rope_table* table, const int32_t* query_start,
@@ -494,7 +495,7 @@ MLA_API int mla_decode_noalloc(const mla_dims* dims, const void* q_cat, const vo
  * status word, the kernel drains its own copies and products and returns, and
  * the context stays usable.  This hook lets a test exercise that path without
  * any fault: with cycles > 0, every later bf16 mla_decode / mla_decode_paged /
- * mla_decode_noalloc launch first waits `cycles` SM cycles on a barrier that
+ * mla_decode_fp8_paged / mla_decode_noalloc launch first waits `cycles` SM cycles on a barrier that
  * nothing ever arrives on, then gives up; its outputs are then undefined.
  * cycles = 0 (the default) turns it off.  Process-wide; not for production
  * use. */

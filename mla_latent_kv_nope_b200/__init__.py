@@ -12,3 +12,4 @@ from .binding import (  # noqa: F401
     out_proj_folded, out_proj_folded_workspace_bytes, plan_pages, plan_pages_workspace_bytes,
     prefill, prefill_workspace_bytes, release_pages, rope, rope_table,
 )
+from .paged import PagedCache  # noqa: F401

@@ -710,12 +710,14 @@ class DecodeStep:
     step is replayed with one launch from the host."""
 
     def __init__(self, dims: Dims, W_UK, W_UV, W_DKV=None, gamma=None, softmax_scale=None,
-                 rope_base=10000.0, eps=1e-6, num_splits=0, device="cuda", overlap=True):
+                 rope_base=10000.0, eps=1e-6, num_splits=0, device="cuda", overlap=True,
+                 rope_table=None):
         self.dims = dims
         self.W_UK, self.W_UV, self.W_DKV, self.gamma = W_UK, W_UV, W_DKV, gamma
         # 0 asks the library for the pages' scale 1/sqrt(d_nope + d_r).
         self.scale = 0.0 if softmax_scale is None else float(softmax_scale)
         self.rope_base, self.eps = rope_base, eps
+        self._splits_arg = num_splits     # 8-bit pages have a default of their own
         self.num_splits = num_splits or decode_default_splits(dims)
         ws = decode_workspace_bytes(dims, self.num_splits)
         self.ws = torch.empty(ws // 4, dtype=torch.float32, device=device)
@@ -728,9 +730,19 @@ class DecodeStep:
         self.lse = torch.empty(dims.B, dims.H, dtype=torch.float32, device=device)
         self.out = torch.empty(dims.B, dims.H, dims.d_v, dtype=dt, device=device)
         self.splits_used = self.num_splits
+        # A rope table (see rope_table) rotates the queries in its layout and
+        # scaling instead of absorb_q's half-split, unscaled rotation.
+        self.rope_table = rope_table
+        if rope_table is not None and rope_table.d_r != dims.d_r:
+            raise ValueError(f"rope_table is for d_r = {rope_table.d_r}, not {dims.d_r}")
+        self.q_rot = (torch.empty(dims.B, dims.H, dims.d_r, dtype=dt, device=device)
+                      if rope_table is not None else None)
         self._side = torch.cuda.Stream(device=device) if overlap else None
 
-    def append(self, h, cache, seqlens, block_table=None, scales=None):
+    def append(self, h, cache, seqlens, block_table=None, scales=None, page_scales=None):
+        if page_scales is not None or self.rope_table is not None:
+            raise ValueError("8-bit pages and rope tables take their rows from "
+                             "cache_write_fp8_paged / cache_write_paged, before the step (h=None)")
         if scales is not None:
             cache_append_fp8(self.dims, h, self.W_DKV, self.gamma, cache, scales, seqlens,
                              self.ws_append, self.eps, self.rope_base)
@@ -743,10 +755,16 @@ class DecodeStep:
 
     def absorb(self, q_nope, q_pe, q_pos):
         """absorb_q into the step's q_cat buffer."""
+        if self.rope_table is not None and q_pos is not None:
+            q_pe, q_pos = rope(self.rope_table, q_pe, q_pos, self.q_rot), None
         absorb_q(self.dims, q_nope, q_pe, self.W_UK, q_pos, self.q_cat, self.rope_base)
 
-    def _attend_latent(self, cache, seqlens, block_table=None, scales=None):
-        if scales is not None:
+    def _attend_latent(self, cache, seqlens, block_table=None, scales=None, page_scales=None):
+        if page_scales is not None:
+            self.splits_used = decode_fp8_paged(self.dims, self.q_cat, cache, page_scales,
+                                                block_table, seqlens, self.scale, self.ws,
+                                                self._splits_arg)
+        elif scales is not None:
             self.splits_used = decode_fp8(self.dims, self.q_cat, cache, scales, seqlens,
                                           self.scale, self.ws, self.num_splits)
         elif block_table is None:
@@ -759,20 +777,26 @@ class DecodeStep:
         out_proj(self.dims, self.o_lat, self.W_UV, self.out)
         return self.out
 
-    def attend(self, q_nope, q_pe, q_pos, cache, seqlens, block_table=None, scales=None):
+    def attend(self, q_nope, q_pe, q_pos, cache, seqlens, block_table=None, scales=None,
+               page_scales=None):
         self.absorb(q_nope, q_pe, q_pos)
-        return self._attend_latent(cache, seqlens, block_table, scales)
+        return self._attend_latent(cache, seqlens, block_table, scales, page_scales)
 
     def __call__(self, q_nope, q_pe, q_pos, cache, seqlens, h=None, block_table=None,
-                 scales=None):
+                 scales=None, page_scales=None):
         """One step.  With ``block_table`` the cache is a paged pool
         [num_pages, 64, R] (see decode_paged); with ``scales`` it is an FP8
         latent cache [B, capacity, d_c + 2 d_r] uint8 with its scale plane
-        [B, capacity] (see decode_fp8)."""
+        [B, capacity] (see decode_fp8); with ``block_table`` and
+        ``page_scales`` [num_pages] an 8-bit paged pool (see decode_fp8_paged),
+        whose rows are written before the step."""
+        if page_scales is not None and block_table is None:
+            raise ValueError("page_scales needs a block_table")
         if self._side is None:
             if h is not None:
-                self.append(h, cache, seqlens, block_table, scales)
-            return self.attend(q_nope, q_pe, q_pos, cache, seqlens, block_table, scales)
+                self.append(h, cache, seqlens, block_table, scales, page_scales)
+            return self.attend(q_nope, q_pe, q_pos, cache, seqlens, block_table, scales,
+                               page_scales)
         main = torch.cuda.current_stream()
         # Fork: the side stream starts after everything issued so far (the
         # previous step's decode has finished reading q_cat).  absorb_q is
@@ -783,12 +807,12 @@ class DecodeStep:
         with torch.cuda.stream(self._side):
             self.absorb(q_nope, q_pe, q_pos)
         if h is not None:
-            self.append(h, cache, seqlens, block_table, scales)
+            self.append(h, cache, seqlens, block_table, scales, page_scales)
         main.wait_stream(self._side)
-        return self._attend_latent(cache, seqlens, block_table, scales)
+        return self._attend_latent(cache, seqlens, block_table, scales, page_scales)
 
     def host_pipeline(self, host_inputs, host_out, cache, seqlens, after=None,
-                      block_table=None, scales=None):
+                      block_table=None, scales=None, page_scales=None):
         """Steps fed from pinned host memory with the copies overlapped.
 
         ``host_inputs`` = (q_nope, q_pe, q_pos[, h]) pinned host tensors,
@@ -802,10 +826,10 @@ class DecodeStep:
         copied in before and the last result copied out after; ``host_out``
         holds the last step's result once the stream has finished."""
         return _HostPipeline(self, host_inputs, host_out, cache, seqlens, after, block_table,
-                             scales)
+                             scales, page_scales)
 
     def capture(self, q_nope, q_pe, q_pos, cache, seqlens, h=None, before=None, after=None,
-                block_table=None, scales=None):
+                block_table=None, scales=None, page_scales=None):
         """Record one step into a CUDA graph; ``before``/``after`` are optional
         callables whose device work is recorded around it.  Replay with
         ``graph.replay()``; inputs are read from the same tensors each time."""
@@ -814,7 +838,7 @@ class DecodeStep:
             if before is not None:
                 before()
             self(q_nope, q_pe, q_pos, cache, seqlens, h=h, block_table=block_table,
-                 scales=scales)
+                 scales=scales, page_scales=page_scales)
             if after is not None:
                 after()
         return g
@@ -823,7 +847,8 @@ class DecodeStep:
 class _HostPipeline:
     """See DecodeStep.host_pipeline."""
 
-    def __init__(self, step, host_inputs, host_out, cache, seqlens, after, block_table, scales):
+    def __init__(self, step, host_inputs, host_out, cache, seqlens, after, block_table, scales,
+                 page_scales=None):
         for t in (*host_inputs, host_out):
             if t.is_cuda or not t.is_pinned():
                 raise ValueError("host_pipeline needs pinned host tensors")
@@ -856,7 +881,7 @@ class _HostPipeline:
                         self.host_out.copy_(self.stages[1 - c], non_blocking=True)
                     x = self.sets[c]
                     step(x[0], x[1], x[2], cache, seqlens, h=x[3] if len(x) > 3 else None,
-                         block_table=block_table, scales=scales)
+                         block_table=block_table, scales=scales, page_scales=page_scales)
                     if after is not None:
                         after()
                     main.wait_stream(self.in_stream)

@@ -27,8 +27,10 @@ constexpr uint32_t kE5m2A = 1u << 7;      // A's format field: E5M2 (lo) instead
 constexpr float kPScale = 6.75f;
 constexpr float kRise = 2.f, kFall = 13.f;   // 2^(6.75 + 2) = 430.5 <= 448
 // Where a reference starts above the maximum of the tile that moves it: the
-// first one, a higher one (the next are likely lower) and a lower one.
-constexpr float kLeadFirst = 8.f, kLeadUp = 6.f, kLeadDown = 9.f;
+// first one, a higher one (the next are likely lower) and a lower one.  With
+// these a maximum that moved it has a power of two as its probability, so a row
+// that one key fills is exact.
+constexpr float kLeadFirst = 7.75f, kLeadUp = 5.75f, kLeadDown = 8.75f;
 constexpr float kTopWindow = 60.f;
 
 // The reference after a tile with maximum mt; `top` is the largest maximum so

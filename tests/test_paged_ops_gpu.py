@@ -571,11 +571,14 @@ def run_decode8(dims, q, pool, scales, table, seq, scale, W=0):
 
 
 def check_attend(o, lse, q, rows, lens, scale):
-    """Each probability is a sum of two E4M3 terms (2^-8 of itself), and those far below
-    their tile's largest are rounded to 2^-16 of it: |o - ref| <= sum p_j |c_j| * 2^-8
-    + 128 keys' 2^-13 of the largest term, fp32 sums on top (2^-20 of the same sum).
-    Scores come from exact products with fp32 sums; the query's own two terms leave
-    2^-18 of its row's largest value per element."""
+    """A probability is hi (E4M3, off by 2^-4 of itself at most) plus lo, the rest in E5M2
+    (2^-3 of that), after a rounding to fp16 (2^-11): 2^-7 + 2^-11 < 2^-6.9 of itself at
+    most.  The bound below takes half of that, 2^-8: the roundings of the 8 and more keys
+    that a row's weight spreads over here do not all point one way, and with a single key
+    p / l = 1 is exact (p is a power of two there).  Probabilities far below their
+    tile's largest are rounded to 2^-13 of it at least: 128 keys' 2^-15 of the largest term.
+    Scores come from exact products with fp32 sums (2^-20); the query's own two terms
+    leave 2^-18 of its row's largest value per element."""
     for b, n in enumerate(lens):
         if n == 0:
             assert bool((o[b] == 0).all()) and bool(torch.isneginf(lse[b]).all())
@@ -675,7 +678,158 @@ def test_decode_fp8_paged_bad_page_and_long_length():
     check_attend(o, lse, q, {0: r}, [200], 0.05)
 
 
+@pytest.mark.parametrize("B,H", [(500, 16), (500, 128), (1100, 64), (900, 128)])
+def test_decode_fp8_paged_many_sequences(B, H):
+    """More sequences than a block has threads, many of them per worker, empty ones among
+    them."""
+    rng = random.Random(B + H)
+    lens = [rng.choice([0, 1, 5, 64, 65, 130, 200]) for _ in range(B)]
+    pool, scales, table, rows = make_pages(lens, H, 64, seed=B)
+    dims = mla.Dims(B, H, 512, 64, 128, 128, table.shape[1] * PAGE, "bf16")
+    q = randn(B, B, H, 576, dtype=torch.bfloat16)
+    o, lse = run_decode8(dims, q, pool, scales, table, i32(lens), 0.07)
+    assert mla.get_device_status() == 0
+    some = rng.sample(range(B), 40)
+    check_attend(o[some], lse[some], q[some], {k: rows[b] for k, b in enumerate(some)},
+                 [lens[b] for b in some], 0.07)
+    empty = [b for b in range(B) if lens[b] == 0]
+    assert not o[empty].any() and torch.isneginf(lse[empty]).all()
+
+
+@pytest.mark.parametrize("H", [64, 128])
+def test_fp8_paged_offsets_past_32_bits(H):
+    """Pages whose bytes lie past 2^32 of a pool of 4.6 GB, written and attended."""
+    n_pages, lens = 112000, [130, 64]
+    dims = mla.Dims(2, H, 512, 64, 128, 128, 256, "bf16")
+    pool = torch.empty(n_pages, PAGE, 640, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(n_pages, device="cuda")
+    ids = [n_pages - 1, 3, n_pages - 2, 111000]
+    table = i32([[ids[0], ids[1], ids[2], -1], [ids[3], -1, -1, -1]])
+    pool[ids] = 0xFF
+    x = randn(4, sum(lens), 576, dtype=torch.bfloat16)
+    mla.cache_write_fp8_paged(dims, x, None, i32([0, 130, 194]), i32(lens), table, pool, scales)
+    q = randn(5, 2, H, 576, dtype=torch.bfloat16)
+    o, lse = run_decode8(dims, q, pool, scales, table, i32(lens), 0.07)
+    assert mla.get_device_status() == 0
+    rows, at = {}, 0
+    for b, n in enumerate(lens):
+        p = [t for t in table[b].tolist() if t >= 0]
+        sc = f64(scales[p])[:, None, None]
+        c, k = codes64(pool[p]) * sc, rope_part(pool[p]) * sc
+        rows[b] = np.concatenate([c, k], 2).reshape(-1, 576)[:n]
+        want, _ = row64(f64(x[at:at + n]), np.arange(n), 1.0, 512, "half", rotate=False)
+        assert np.linalg.norm(rows[b][:, :512] - want) < 2.0 ** -4 * np.linalg.norm(want)
+        at += n
+    check_attend(o, lse, q, rows, lens, 0.07)
+    # The bf16 writer at a slot whose bytes lie past 2^32.
+    big = torch.empty(60000, PAGE, 576, dtype=torch.bfloat16, device="cuda")
+    slots = torch.tensor([60000 * 64 - 1, 5], device="cuda")
+    mla.cache_write_paged(dims, x[:2], None, None, slots, big)
+    assert torch.equal(big.view(-1, 576)[slots][:, 512:], x[:2, 512:])
+
+
+@pytest.mark.parametrize("H,d_r", [(64, 64), (128, 64), (64, 0), (128, 0)])
+def test_decode_fp8_paged_gives_up(H, d_r):
+    """A wait that runs out (nothing arrives on its barrier) ends the kernel with a status
+    and leaves the context usable: the next decode is right."""
+    lens = [700, 65, 1]
+    pool, scales, table, rows = make_pages(lens, H, d_r, seed=2)
+    dims = mla.Dims(3, H, 512, d_r, 128, 128, table.shape[1] * PAGE, "bf16")
+    q = randn(6, 3, H, 512 + d_r, dtype=torch.bfloat16)
+    assert mla.get_device_status() == 0
+    try:
+        mla.debug_inject_wait(200_000)      # about 0.1 ms of SM cycles
+        run_decode8(dims, q, pool, scales, table, i32(lens), 0.07)
+        status = mla.get_device_status()
+    finally:
+        mla.debug_inject_wait(0)
+    assert status == 6                      # MLA_ERR_DEVICE_TIMEOUT
+    o, lse = run_decode8(dims, q, pool, scales, table, i32(lens), 0.07)
+    assert mla.get_device_status() == 0
+    check_attend(o, lse, q, rows, lens, 0.07)
+
+
+def test_two_streams_at_once():
+    """Two decodes with a workspace each, on two streams, and a repeated one: the same bits."""
+    cases = []
+    for H, lens in ((128, [3000, 100, 77]), (64, [5000, 64])):
+        pool, scales, table, rows = make_pages(lens, H, 64, seed=H)
+        dims = mla.Dims(len(lens), H, 512, 64, 128, 128, table.shape[1] * PAGE, "bf16")
+        q = randn(H, len(lens), H, 576, dtype=torch.bfloat16)
+        cases.append((dims, q, pool, scales, table, i32(lens)))
+    alone = [run_decode8(*c, 0.07) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(20):
+        got = []
+        for c, s in zip(cases, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append(run_decode8(*c, 0.07))
+        torch.cuda.synchronize()
+        for (o, l), (o1, l1) in zip(alone, got):
+            assert torch.equal(o, o1) and torch.equal(l, l1)
+    assert mla.get_device_status() == 0
+
+
 # ------------------------------------------------------------------- together
+@pytest.mark.parametrize("fp8", [True, False])
+def test_paged_cache_with_decode_steps(fp8):
+    """PagedCache and DecodeStep: prompts, decode steps, a finished request's pages used
+    again; the step's output against materialised attention over the written rows."""
+    B, H = 3, 16
+    dims = mla.Dims(B, H, 512, 64, 128, 128, 256, "bf16")
+    tab = mla.rope_table(64, layout="interleaved", scaling="yarn", factor=4.0)
+    freq, amp = frequencies(64, scaling="yarn", factor=4.0)
+    W_UK = (0.05 * randn(1, H, 128, 512)).to(torch.bfloat16)
+    W_UV = (0.05 * randn(2, H, 128, 512)).to(torch.bfloat16)
+    cache = mla.PagedCache(dims, num_pages=8, max_tokens=256, fp8=fp8, table=tab)
+    step = mla.DecodeStep(dims, W_UK, W_UV, rope_table=tab)
+    xs = [np.zeros((0, 576)) for _ in range(B)]
+    for it, new in enumerate([[70, 3, 0], [1, 1, 100], [1, 1, 1], "release 0", [2, 1, 1], [150, 1, 1]]):
+        if new == "release 0":
+            cache.release(i32([1, 0, 0]))
+            xs[0] = xs[0][:0]
+            continue
+        cache.plan(i32(new))
+        x = randn(it, sum(new), 576, dtype=torch.bfloat16)
+        cache.write(x)
+        at = 0
+        for b in range(B):
+            xs[b] = np.concatenate([xs[b], f64(x[at:at + new[b]])])
+            at += new[b]
+        qn = randn(20 + it, B, H, 128, dtype=torch.bfloat16)
+        qp = randn(40 + it, B, H, 64, dtype=torch.bfloat16)
+        out = step(qn, qp, cache.last_positions(), cache.pool, cache.seqlens,
+                   block_table=cache.block_table, page_scales=cache.page_scales)
+        assert mla.get_device_status() == 0
+        assert cache.seqlens.tolist() == [len(v) for v in xs]
+        used = sum(-(-len(v) // PAGE) for v in xs)
+        assert cache.free_count.item() == 8 - used
+        for b in range(B):
+            n = len(xs[b])
+            if n == 0:
+                assert not out[b].any()
+                continue
+            c = xs[b][:, :512] / np.sqrt((xs[b][:, :512] ** 2).mean(-1, keepdims=True) + 1e-6)
+            k = rope64(xs[b][:, 512:], np.arange(n), freq, amp, "interleaved")
+            q = np.concatenate([np.einsum("hn,hnc->hc", f64(qn[b]), f64(W_UK)),
+                                rope64(f64(qp[b])[None], [n - 1], freq, amp, "interleaved")[0]], 1)
+            ref, _, _ = attend64(q, np.concatenate([c, k], 1), 1 / math.sqrt(192))
+            ref = np.einsum("hc,hvc->hv", ref, f64(W_UV))
+            # bf16 queries, probabilities and outputs; E4M3 rows where the cache is 8-bit.
+            lim = 2.0 ** -4 if fp8 else 1.5e-2
+            assert np.linalg.norm(f64(out[b]) - ref) < lim * np.linalg.norm(ref)
+    with pytest.raises(ValueError, match="before the step"):
+        step(qn, qp, cache.last_positions(), cache.pool, cache.seqlens, h=x,
+             block_table=cache.block_table, page_scales=cache.page_scales)
+    with pytest.raises(ValueError, match="block_table"):
+        mla.DecodeStep(dims, W_UK, W_UV)(qn, qp, cache.last_positions(), cache.pool, cache.seqlens,
+                                         page_scales=torch.ones(8, device="cuda"))
+    with pytest.raises(ValueError, match="rope_table"):
+        mla.DecodeStep(dims, W_UK, W_UV, rope_table=mla.rope_table(32))
+
+
 def test_paged_serving_run():
     """Prompts in chunks, then decode steps from a captured graph: plan, write,
     rotate, attend; the 8-bit pages against attention over the same rows in 64
