@@ -8,7 +8,9 @@ library raises immediately -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import dataclasses
 import functools
+import importlib.util
 import os
 from dataclasses import dataclass
 
@@ -87,12 +89,20 @@ class Dims:
                      self.cache_capacity, MLA_BF16 if self.dtype == "bf16" else MLA_F32)
 
     @functools.cached_property
+    def _struct(self):
+        return self.c()      # made once: the fields are frozen
+
+    @functools.cached_property
     def ref(self):
-        """A reference to the C struct, made once (the fields are frozen)."""
-        return ctypes.byref(self.c())
+        """A reference to the C struct."""
+        return ctypes.byref(self._struct)
+
+    @functools.cached_property
+    def address(self) -> int:
+        return ctypes.addressof(self._struct)
 
     def __getstate__(self):
-        return {k: v for k, v in self.__dict__.items() if k != "ref"}
+        return {f.name: getattr(self, f.name) for f in dataclasses.fields(self)}
 
     @property
     def torch_dtype(self):
@@ -104,6 +114,7 @@ class Dims:
 
 
 _lib = None
+_calls = None     # the checks and calls of the short operators in C++ (csrc/py_calls.cpp)
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -165,7 +176,22 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         fn.restype = res
         fn.argtypes = args
     _lib = lib
+    _load_calls(lib)
     return lib
+
+
+def _load_calls(lib) -> None:
+    global _calls
+    at = os.path.join(_HERE, "_calls.so")
+    if not os.path.exists(at):
+        raise RuntimeError(f"{at} is missing: build it with mla_latent_kv_nope_b200.build.build()")
+    spec = importlib.util.spec_from_file_location("_calls", at)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.init(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+        "mla_rope", "mla_plan_pages", "mla_cache_write_paged", "mla_cache_write_fp8_paged",
+        "mla_decode_fp8_paged")))
+    _calls = mod
 
 
 def _check(fn: str, status: int):
@@ -485,8 +511,10 @@ def out_proj_folded(dims: Dims, o_lat, W_fold, u, workspace, stream=None):
 
 # ---------------------------------------------------------------------------
 # Paged serving: rotary positions, page plans, writes of many tokens, 8-bit pages.
-# Their kernels take a few microseconds, so these wrappers keep the host's part
-# short: one look at each tensor, raw pointers and streams.
+# Their kernels take a few microseconds, so the host's part is short too: a call on
+# the current device and stream goes to _calls, which checks the tensors in C++ and
+# makes it, or answers None where something is amiss (or on another device or stream);
+# then the checks here say what, or make the call through ctypes.
 _ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 _ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 _I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
@@ -577,6 +605,10 @@ def rope(table: RopeTable, x, pos, out=None, transpose=False, stream=None):
     gradient of the rotation's output taken back to its input)."""
     if not isinstance(table, RopeTable):
         raise TypeError("table must come from rope_table()")
+    if _calls is not None and out is not None and stream is None:
+        st = _calls.rope(table, x, pos, out, transpose)
+        if st is not None:
+            return out if st == 0 else _check("mla_rope", st)
     dev = _device(x, "x")
     shape, st, dt = x.shape, x.stride(), x.dtype
     n = len(shape)
@@ -611,6 +643,12 @@ def plan_pages(seqlens, new_lens, block_table, free_pages, free_count, num_pages
     list into block_table [B, max_blocks], and fill query_start [B+1],
     positions [T] (int32) and slots [T] (int64); seqlens_out and
     free_count_out may be seqlens and free_count."""
+    if _calls is not None and stream is None:
+        st = _calls.plan_pages(seqlens, new_lens, block_table, free_pages, free_count, num_pages,
+                               query_start, positions, slots, seqlens_out, free_count_out,
+                               workspace, token_request)
+        if st is not None:
+            return _check("mla_plan_pages", st) if st else None
     dev = _device(seqlens, "seqlens")
     B, T, F = seqlens.shape[0], positions.shape[0], free_pages.numel()
     mb = block_table.shape[-1]
@@ -645,6 +683,11 @@ def cache_write_paged(dims: Dims, x, gamma, positions, slots, cache_pool, table=
     """mla_cache_write_paged: the rows [RMSNorm(x_c) * gamma || RoPE(x_r, position)] of
     projected tokens x [T, d_c + d_r] to rows ``slots`` (int64, -1: none) of
     cache_pool [num_pages, 64, d_c + d_r].  Without a table x_r is stored as it is."""
+    if _calls is not None and stream is None:
+        st = _calls.cache_write_paged(dims.address, x, gamma, positions, slots, cache_pool, table,
+                                      eps)
+        if st is not None:
+            return _check("mla_cache_write_paged", st) if st else None
     dev = _device(x, "x")
     dt, R, n = dims.torch_dtype, dims.R, cache_pool.shape[0]
     px, T, sx = _rows(x, dt, R, dev)
@@ -662,6 +705,11 @@ def cache_write_fp8_paged(dims: Dims, x, gamma, query_start, seqlens, block_tabl
     [num_pages, 64, d_c + 2 d_r] uint8 with one scale per page [num_pages];
     request b's rows are x[query_start[b]:query_start[b+1]], the last of its
     seqlens[b] tokens (the lengths after the step)."""
+    if _calls is not None and stream is None:
+        st = _calls.cache_write_fp8_paged(dims.address, x, gamma, query_start, seqlens, block_table,
+                                          cache_pool, page_scales, table, eps)
+        if st is not None:
+            return _check("mla_cache_write_fp8_paged", st) if st else None
     dev = _device(x, "x")
     B, n, mb = dims.B, cache_pool.shape[0], block_table.shape[-1]
     px, T, sx = _rows(x, dims.torch_dtype, dims.R, dev)
@@ -678,6 +726,11 @@ def decode_fp8_paged(dims: Dims, q_cat, cache_pool, page_scales, block_table, se
                      softmax_scale, workspace, num_splits=0, stream=None) -> int:
     """mla_decode_fp8_paged: mla_decode over an 8-bit paged cache (see
     cache_write_fp8_paged); returns the splits used, for combine."""
+    if _calls is not None and stream is None:
+        got = _calls.decode_fp8_paged(dims.address, q_cat, cache_pool, page_scales, block_table,
+                                      seqlens, softmax_scale, workspace, num_splits)
+        if got is not None:
+            return got if got > 0 else _check("mla_decode_fp8_paged", -got)
     dev = _device(q_cat, "q_cat")
     B, n, mb = dims.B, cache_pool.shape[0], block_table.shape[-1]
     ws, nws = _ws_arg(workspace, dev)
