@@ -19,25 +19,27 @@ namespace mla {
 namespace {
 
 constexpr int kPlanThreads = 256;
-constexpr int kPlanTokens = 1024;   // tokens per block
+constexpr int kPlanTokens = 512;    // tokens per block
 
 __device__ __forceinline__ int64_t pages_of(int64_t L) { return (L + kTileKeys - 1) / kTileKeys; }
 
-// Sum over the block of a 64-bit value (every thread gets it).  `red` holds
-// one value per warp; two barriers.
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* red) {
+// Sums over the block of two 64-bit values, and whether any thread's `bad` is
+// set (every thread gets them; one barrier).
+__device__ __forceinline__ void block_sum2(int64_t& a, int64_t& b, int& bad,
+                                           int64_t (*red)[2]) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int64_t s = 0;
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5][0] = a, red[threadIdx.x >> 5][1] = b;
+  bad = __syncthreads_or(bad);
+  a = b = 0;
 #pragma unroll
-  for (int w = 0; w < kPlanThreads / 32; ++w) s += red[w];
-  return s;
+  for (int w = 0; w < kPlanThreads / 32; ++w) a += red[w][0], b += red[w][1];
 }
 
-// Inclusive prefix over the block of two values.
+// Inclusive prefix over the block of two values (one barrier).
 __device__ __forceinline__ void block_scan2(int32_t& a, int32_t& b, int32_t (*red)[2]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -45,7 +47,6 @@ __device__ __forceinline__ void block_scan2(int32_t& a, int32_t& b, int32_t (*re
     const int32_t ua = __shfl_up_sync(0xffffffffu, a, o), ub = __shfl_up_sync(0xffffffffu, b, o);
     if (lane >= o) a += ua, b += ub;
   }
-  __syncthreads();
   if (lane == 31) red[warp][0] = a, red[warp][1] = b;
   __syncthreads();
 #pragma unroll
@@ -86,7 +87,7 @@ struct PlanArgs {
 };
 
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs a) {
-  __shared__ int64_t s_red[kPlanThreads / 32];
+  __shared__ int64_t s_red[kPlanThreads / 32][2];
   __shared__ int32_t s_red2[kPlanThreads / 32][2];
   __shared__ int32_t s_tok[kPlanThreads], s_page[kPlanThreads];   // ends of each request's share
   __shared__ int32_t s_len[kPlanThreads], s_new[kPlanThreads];
@@ -96,16 +97,18 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
   const int32_t free_n = *a.free_count;
 
   // Totals and checks: a step that cannot be served as a whole is not begun.
+  // The first kPlanThreads requests stay in registers for the second walk.
   int64_t tok = 0, need = 0;
   int bad = 0;
+  int32_t L0 = 0, n0 = 0;
   for (int b = tid; b < a.B; b += kPlanThreads) {
-    const int64_t L = a.seqlens[b], n = a.new_lens[b];
+    const int32_t Lb = a.seqlens[b], nb = a.new_lens[b];
+    if (b == tid) L0 = Lb, n0 = nb;
+    const int64_t L = Lb, n = nb;
     if (L < 0 || n < 0 || L + n > int64_t(a.max_blocks) * kTileKeys || L + n > INT32_MAX) bad = 1;
     else tok += n, need += pages_of(L + n) - pages_of(L);
   }
-  bad = __syncthreads_or(bad);
-  tok = block_sum(tok, s_red);
-  need = block_sum(need, s_red);
+  block_sum2(tok, need, bad, s_red);
   if (tok > a.T || need > free_n || free_n < 0 || free_n > a.free_capacity) bad = 1;
   if (bad) tok = need = 0;
 
@@ -119,7 +122,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     // Block 0 writes query_start for every request, so it walks them all.
     if (blockIdx.x && tok_base >= live1 && page_base >= p1) break;
     const int b = b0 + tid;
-    const int32_t L = b < a.B ? a.seqlens[b] : 0, n = b < a.B ? a.new_lens[b] : 0;
+    const bool in_regs = b0 == 0;
+    const int32_t L = in_regs ? L0 : b < a.B ? a.seqlens[b] : 0;
+    const int32_t n = in_regs ? n0 : b < a.B ? a.new_lens[b] : 0;
     int32_t te = n, pe = int32_t(pages_of(int64_t(L) + n) - pages_of(L));
     block_scan2(te, pe, s_red2);
     te += tok_base, pe += page_base;
