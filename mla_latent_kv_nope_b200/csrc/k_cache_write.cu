@@ -41,6 +41,15 @@ __device__ __forceinline__ uint4 pack16(const float (&f)[kVec]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Two fp32 products in one instruction.
+__device__ __forceinline__ void mul2(float* a, float bx, float by) {
+  asm("{\n\t.reg .b64 ra, rb;\n\t"
+      "mov.b64 ra, {%0, %1};\n\tmov.b64 rb, {%2, %3};\n\t"
+      "mul.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+      : "+f"(a[0]), "+f"(a[1])
+      : "f"(bx), "f"(by));
+}
+
 __device__ __forceinline__ void load_gamma(const float* gamma, int c, int n, float* g) {
 #pragma unroll
   for (int i = 0; i < n; i += 4) {
@@ -277,8 +286,13 @@ cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
 #pragma unroll
     for (int e = 0; e < 16; ++e) ss = fmaf(f[e], f[e], ss);
     const float inv = rsqrtf(warp_sum(ss) * (1.f / k8Dc) + eps);
+    float top = 0.f;     // the row's largest |x gamma|; its factor is common and positive
 #pragma unroll
-    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(f[e] * inv * g[e]));
+    for (int e = 0; e < 16; e += 2) {
+      mul2(f + e, g[e], g[e + 1]);
+      top = fmaxf(top, fmaxf(fabsf(f[e]), fabsf(f[e + 1])));
+    }
+    amax = fmaxf(amax, top * inv);
     if (lane == 0) s_inv[r] = inv;
   }
   amax = warp_max(amax);
@@ -319,7 +333,10 @@ cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
     float f[16];
     row_values(r, f);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) f[e] = f[e] * inv * g[e];
+    for (int e = 0; e < 16; e += 2) {
+      mul2(f + e, g[e], g[e + 1]);
+      mul2(f + e, inv, inv);
+    }
     reinterpret_cast<uint2*>(row)[lane] =
         make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
     reinterpret_cast<uint2*>(row)[lane + 32] =
