@@ -199,18 +199,41 @@ __device__ __forceinline__ int query_exponent(uint32_t top) {
 }
 __device__ __forceinline__ float exp2i(int k) { return __uint_as_float(uint32_t(127 + k) << 23); }
 
-// One word of two bf16 values times inv, as two E4M3 terms of two codes each.
-__device__ __forceinline__ void split_query(uint32_t w, float inv, uint32_t* hi, uint32_t* lo) {
-  const __half2 x = __floats2half2_rn(__uint_as_float(w << 16) * inv,
-                                      __uint_as_float(w & 0xFFFF0000u) * inv);
+// The larger of each half of two words of bf16 magnitudes (sign bits cleared), and
+// the larger half of one.
+__device__ __forceinline__ uint32_t max_magnitude2(uint32_t top2, uint32_t w) {
+  return __vmaxu2(top2, w & 0x7FFF7FFFu);
+}
+__device__ __forceinline__ uint32_t larger_half(uint32_t top2) {
+  return max(top2 & 0xFFFFu, top2 >> 16);
+}
+
+// One word of two bf16 values times the power of two inv2 (bf16 in both halves:
+// exact), as two E4M3 terms of two codes each, through fp16 (exact down to 2^-14).
+__device__ __forceinline__ void split_query(uint32_t w, __nv_bfloat162 inv2, uint32_t* hi,
+                                            uint32_t* lo) {
+  const __nv_bfloat162 s = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), inv2);
+  const uint32_t b = *reinterpret_cast<const uint32_t*>(&s);
+  const __half2 x = __floats2half2_rn(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u));
   *hi = __nv_cvt_halfraw2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
   const __half2 back(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(*hi), __NV_E4M3));
   *lo = __nv_cvt_halfraw2_to_fp8x2(__hsub2(x, back), __NV_SATFINITE, __NV_E4M3);
 }
-__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t w, float inv) {
-  const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(w << 16) * inv,
-                                                 __uint_as_float(w & 0xFFFF0000u) * inv);
-  return *reinterpret_cast<const uint32_t*>(&p);
+// The RoPE part of a query row in the same units.
+__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t w, __nv_bfloat162 inv2) {
+  const __nv_bfloat162 s = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), inv2);
+  return *reinterpret_cast<const uint32_t*>(&s);
+}
+
+// This CTA's share of the queries into L2, before the lengths say which of them
+// it needs (one thread): all CTAs together ask for each row once, and the first
+// query block is then read from L2 instead of from memory behind a TLB miss.
+__device__ __forceinline__ void prefetch_queries(const __nv_bfloat16* q_cat, int64_t bytes,
+                                                 int64_t cta, int64_t n_cta) {
+  const int64_t share = ((bytes + n_cta - 1) / n_cta + 15) / 16 * 16;
+  const int64_t at = cta * share, end = min(at + share, bytes);
+  if (at < end)
+    bulk_prefetch_l2(reinterpret_cast<const char*>(q_cat) + at, uint32_t(end - at));
 }
 
 // Page rows and scales of a run of tiles: lane l holds tile base + l, and the

@@ -122,6 +122,9 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
 
   pdl_wait();
   // Asked for before the setup that it does not depend on.
+  if (threadIdx.x == 32 * kKWarp)
+    prefetch_queries(q_cat, int64_t(B) * H * R * 2, int64_t(blockIdx.y) * gridDim.x + blockIdx.x,
+                     int64_t(gridDim.x) * gridDim.y);
   const int32_t len0 = int(threadIdx.x) < B ? seqlens[threadIdx.x] : 0;
   if (threadIdx.x == 0) {
     // The leader's also wait for the other CTA's word that its stage has landed.
@@ -369,7 +372,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
 #pragma unroll 1
       for (int r0 = 0; r0 < 8; r0 += 2) {
         uint32_t wd[2][8], rd[2][4], top[2] = {0, 0};
-        float inv[2];
+        __nv_bfloat162 inv[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const uint4 v0 = u[r][0], v1 = u[r][1], vr = ur[r];
@@ -378,16 +381,15 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
           rd[r][0] = vr.x, rd[r][1] = vr.y, rd[r][2] = vr.z, rd[r][3] = vr.w;
           // Largest magnitude of the row: bf16 bits order like their magnitudes.
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
-            top[r] = max(top[r], max(wd[r][x] & 0x7FFFu, (wd[r][x] >> 16) & 0x7FFFu));
+          for (int x = 0; x < 8; ++x) top[r] = max_magnitude2(top[r], wd[r][x]);
         }
 #pragma unroll
         for (int e = 0; e < 6; ++e) u[e][0] = u[e + 2][0], u[e][1] = u[e + 2][1], ur[e] = ur[e + 2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          top[r] = __reduce_max_sync(0xffffffffu, top[r]);
+          top[r] = __reduce_max_sync(0xffffffffu, larger_half(top[r]));
           const int k = query_exponent(top[r]);
-          inv[r] = exp2i(-k);
+          inv[r] = __float2bfloat162_rn(exp2i(-k));
           if (lane == 0) s_row[8 * warp + r0 + r] = exp2i(k);
         }
 #pragma unroll

@@ -72,8 +72,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 decode8_64_kernel(const __grid_constant__ CUtensorMap tm_codes,
                   const __grid_constant__ CUtensorMap tm_rope,
                   const __grid_constant__ CUtensorMap tm_query,
-                  const float* __restrict__ page_scales, const PageMap pm,
-                  const int32_t* __restrict__ seqlens, int B, int H, int64_t cap,
+                  const __nv_bfloat16* __restrict__ q_cat, const float* __restrict__ page_scales,
+                  const PageMap pm, const int32_t* __restrict__ seqlens, int B, int H, int64_t cap,
                   float scale_log2, int W, float* __restrict__ o_part,
                   float* __restrict__ lse_part, int* __restrict__ status, uint64_t inject_wait) {
   constexpr int kQueryChunks = (kDc + kDr) / 64;
@@ -84,6 +84,8 @@ decode8_64_kernel(const __grid_constant__ CUtensorMap tm_codes,
 
   pdl_wait();
   // Asked for before the setup that it does not depend on.
+  if (threadIdx.x == 32 * kProducerWarp)
+    prefetch_queries(q_cat, int64_t(B) * H * (kDc + kDr) * 2, w, W);
   const int32_t len0 = int(threadIdx.x) < B ? seqlens[threadIdx.x] : 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&bars->full[s], 1), mbar_init(&bars->empty[s], 1);
@@ -270,14 +272,14 @@ decode8_64_kernel(const __grid_constant__ CUtensorMap tm_codes,
 #pragma unroll 4
       for (int j = 0; j < 16; ++j) {
         const uint4 a = unit(4 * j + 2 * half), b = unit(4 * j + 2 * half + 1);
-        const uint32_t wd[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         // bf16 bits order like their magnitudes.
-#pragma unroll
-        for (int x = 0; x < 8; ++x) top = max(top, max(wd[x] & 0x7FFFu, (wd[x] >> 16) & 0x7FFFu));
+        top = max_magnitude2(max_magnitude2(max_magnitude2(max_magnitude2(top, a.x), a.y), a.z), a.w);
+        top = max_magnitude2(max_magnitude2(max_magnitude2(max_magnitude2(top, b.x), b.y), b.z), b.w);
       }
+      top = larger_half(top);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
       const int k = query_exponent(top);
-      const float inv = exp2i(-k);
+      const __nv_bfloat162 inv = __float2bfloat162_rn(exp2i(-k));
       row_factor = exp2i(k);
 #pragma unroll 2
       for (int j = 0; j < 16; ++j) {
@@ -480,9 +482,9 @@ cudaError_t launch_decode_fp8_paged64(const CUtensorMap& tm_codes, const CUtenso
     return cudaErrorInvalidValue;
   const dim3 grid(W);
   if (d_r)
-    return launch_t<64>(grid, stream, tm_codes, tm_rope, tm_query, page_scales, pm, seqlens, B, H,
+    return launch_t<64>(grid, stream, tm_codes, tm_rope, tm_query, q_cat, page_scales, pm, seqlens, B, H,
                         cap, scale_log2, W, o_part, lse_part, status, inject_wait);
-  return launch_t<0>(grid, stream, tm_codes, tm_rope, tm_query, page_scales, pm, seqlens, B, H, cap,
+  return launch_t<0>(grid, stream, tm_codes, tm_rope, tm_query, q_cat, page_scales, pm, seqlens, B, H, cap,
                      scale_log2, W, o_part, lse_part, status, inject_wait);
 }
 
