@@ -83,7 +83,7 @@ struct Bars {
   uint64_t vfull[kVStages], vempty[kVStages];
   uint64_t s_full[2], s_free[2];
   uint64_t p_full[2], pv_done[2];
-  uint64_t q_ready, o_free, qk_drain, pv_drain, never;
+  uint64_t q_raw, q_ready, o_free, qk_drain, pv_drain, never;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -107,6 +107,7 @@ template <int kDr>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
                const __grid_constant__ CUtensorMap tm_rope,
+               const __grid_constant__ CUtensorMap tm_query,
                const float* __restrict__ page_scales, const PageMap pm,
                const __nv_bfloat16* __restrict__ q_cat, const int32_t* __restrict__ seqlens, int B,
                int H, int64_t cap, float scale_log2, int W, float* __restrict__ o_part,
@@ -135,6 +136,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
       mbar_init(&bars->vempty[s], 1);
     }
     for (int s = 0; s < 2; ++s) mbar_init(&bars->s_full[s], 1), mbar_init(&bars->s_free[s], 2 * kSoftmaxWarps);
+    mbar_init(&bars->q_raw, 1);
     mbar_init(&bars->q_ready, 2 * kSoftmaxWarps);   // the softmax warps of both CTAs
     mbar_init(&bars->o_free, 2 * kSoftmaxWarps);
     for (int s = 0; s < 2; ++s)
@@ -152,6 +154,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
   }
   if (threadIdx.x == 32 * kKWarp) {
     tma_prefetch_desc(&tm_codes);
+    tma_prefetch_desc(&tm_query);
     if (kDr) tma_prefetch_desc(&tm_rope);
   }
   tc_fence_before();
@@ -355,27 +358,35 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
       if (!ok && lane == 0) raise_abort(bars, status);
     };
 
-    // Splits the query block of sequence b into E4M3 terms: a warp takes 8
-    // rows, all loads in flight at once; the code is two rows' (the loop stays
-    // rolled: unrolled, fetching its instructions took 10 us at every start).
+    // The query block of sequence b (64 rows of q_cat; rows past the sequence's
+    // heads are another's, or zeros past the end: not stored) is copied as bf16
+    // into the shared memory that its E4M3 terms will take, and split in place: a
+    // warp takes 8 rows, two at a time, and has read a row before it writes it.
+    uint32_t n_query = 0;
     auto write_query = [&](int b) {
-      uint4 u[8][2], ur[8];
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const int h = g * kHeadsPerCta + 8 * warp + r;
-        const uint4* src = reinterpret_cast<const uint4*>(q_cat + (int64_t(b) * H + h) * R);
-        const uint4 z = make_uint4(0, 0, 0, 0);
-        u[r][0] = h < H ? src[lane] : z;
-        u[r][1] = h < H ? src[lane + 32] : z;
-        ur[r] = kDr && h < H && lane < kDr / 8 ? src[64 + lane] : z;
+      if (tid == 0 && ok) {
+        fence_proxy_async_smem();   // after what threads have read and written there
+        mbar_arrive_expect_tx(&bars->q_raw, (R / 64) * kChunk);
+#pragma unroll 1
+        for (int c = 0; c < R / 64; ++c)
+          tma_load_2d(&tm_query, &bars->q_raw, smem + kOffQ + c * kChunk, c * 64,
+                      b * H + g * kHeadsPerCta);
       }
+      await(&bars->q_raw, n_query++ & 1);
+      // 16-byte unit un (8 values) of row qr.
+      auto unit = [&](int qr, int un) {
+        return *reinterpret_cast<const uint4*>(smem + kOffQ + (un / 8) * kChunk + qr * 128 +
+                                               (((un % 8) ^ (qr & 7)) * 16));
+      };
 #pragma unroll 1
       for (int r0 = 0; r0 < 8; r0 += 2) {
         uint32_t wd[2][8], rd[2][4], top[2] = {0, 0};
         __nv_bfloat162 inv[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const uint4 v0 = u[r][0], v1 = u[r][1], vr = ur[r];
+          const int qr = 8 * warp + r0 + r;
+          const uint4 v0 = unit(qr, lane), v1 = unit(qr, lane + 32);
+          const uint4 vr = kDr && lane < kDr / 8 ? unit(qr, 64 + lane) : make_uint4(0, 0, 0, 0);
           wd[r][0] = v0.x, wd[r][1] = v0.y, wd[r][2] = v0.z, wd[r][3] = v0.w;
           wd[r][4] = v1.x, wd[r][5] = v1.y, wd[r][6] = v1.z, wd[r][7] = v1.w;
           rd[r][0] = vr.x, rd[r][1] = vr.y, rd[r][2] = vr.z, rd[r][3] = vr.w;
@@ -384,9 +395,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
           for (int x = 0; x < 8; ++x) top[r] = max_magnitude2(top[r], wd[r][x]);
         }
 #pragma unroll
-        for (int e = 0; e < 6; ++e) u[e][0] = u[e + 2][0], u[e][1] = u[e + 2][1], ur[e] = ur[e + 2];
-#pragma unroll
         for (int r = 0; r < 2; ++r) {
+          // (The whole warp has read both rows once it has their maxima.)
           top[r] = __reduce_max_sync(0xffffffffu, larger_half(top[r]));
           const int k = query_exponent(top[r]);
           inv[r] = __float2bfloat162_rn(exp2i(-k));
@@ -587,6 +597,10 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
       tc_fence_before();
       arrive(a_o);
     }
+    if (tid == 0 && n_query) {   // the last copy has landed, after a give-up as well
+      volatile int no_abort = 0;
+      mbar_wait(&bars->q_raw, (n_query - 1) & 1, &no_abort, kWaitLimitCycles / 100);
+    }
   }
   if (!ok && lane == 0) raise_abort(bars, status);
 
@@ -631,7 +645,7 @@ inline int head_pairs(int H) { return (H + 2 * kHeadsPerCta - 1) / (2 * kHeadsPe
 
 // The kernel for up to 64 heads (k_decode_fp8_paged64.cu).
 cudaError_t launch_decode_fp8_paged64(const CUtensorMap& tm_codes, const CUtensorMap& tm_rope,
-                                      const __nv_bfloat16* q_cat, const float* page_scales,
+                                      const CUtensorMap& tm_query, const __nv_bfloat16* q_cat, const float* page_scales,
                                       const PageMap& pm, const int32_t* seqlens, int B, int H,
                                       int d_r, int64_t cap, float scale_log2, int W, float* o_part,
                                       float* lse_part, int* status, uint64_t inject_wait,
@@ -653,21 +667,24 @@ cudaError_t launch_decode_fp8_paged(const __nv_bfloat16* q_cat, const uint8_t* p
   if (!make_code_map(&tm_codes, pool, rows, row_bytes)) return cudaErrorInvalidValue;
   tm_rope = tm_codes;
   // The same rows viewed as bf16: the RoPE keys are columns 256 .. 319.
+  CUtensorMap tm_query;
+  if (!make_map16(&tm_query, q_cat, uint64_t(B) * H, uint64_t(kDc + d_r), uint64_t(kDc + d_r), 64))
+    return cudaErrorInvalidValue;
   if (d_r && !make_map16(&tm_rope, pool, rows, row_bytes / 2, row_bytes / 2, kTileKeys))
     return cudaErrorInvalidValue;
   const float scale_log2 = scale * 1.4426950408889634f;
   if (H <= kHeadsPerCta)   // a pair's second CTA would have no heads
-    return launch_decode_fp8_paged64(tm_codes, tm_rope, q_cat, page_scales, pm, seqlens, B, H, d_r,
+    return launch_decode_fp8_paged64(tm_codes, tm_rope, tm_query, q_cat, page_scales, pm, seqlens, B, H, d_r,
                                      cap, scale_log2, W, o_part, lse_part, status, inject_wait,
                                      stream);
   const dim3 grid(2 * head_pairs(H), W);
-  auto launch = d_r ? launch_t<64, CUtensorMap, CUtensorMap, const float*, PageMap,
+  auto launch = d_r ? launch_t<64, CUtensorMap, CUtensorMap, CUtensorMap, const float*, PageMap,
                                const __nv_bfloat16*, const int32_t*, int, int, int64_t, float, int,
                                float*, float*, int*, uint64_t>
-                    : launch_t<0, CUtensorMap, CUtensorMap, const float*, PageMap,
+                    : launch_t<0, CUtensorMap, CUtensorMap, CUtensorMap, const float*, PageMap,
                                const __nv_bfloat16*, const int32_t*, int, int, int64_t, float, int,
                                float*, float*, int*, uint64_t>;
-  return launch(grid, stream, tm_codes, tm_rope, page_scales, pm, q_cat, seqlens, B, H, cap,
+  return launch(grid, stream, tm_codes, tm_rope, tm_query, page_scales, pm, q_cat, seqlens, B, H, cap,
                 scale_log2, W, o_part, lse_part, status, inject_wait);
 }
 

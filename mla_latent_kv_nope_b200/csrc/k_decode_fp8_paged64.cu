@@ -472,14 +472,11 @@ cudaError_t launch_t(dim3 grid, cudaStream_t stream, Args... args) {
 }  // namespace
 
 cudaError_t launch_decode_fp8_paged64(const CUtensorMap& tm_codes, const CUtensorMap& tm_rope,
-                                      const __nv_bfloat16* q_cat, const float* page_scales,
+                                      const CUtensorMap& tm_query, const __nv_bfloat16* q_cat, const float* page_scales,
                                       const PageMap& pm, const int32_t* seqlens, int B, int H,
                                       int d_r, int64_t cap, float scale_log2, int W, float* o_part,
                                       float* lse_part, int* status, uint64_t inject_wait,
                                       cudaStream_t stream) {
-  CUtensorMap tm_query;
-  if (!make_map16(&tm_query, q_cat, uint64_t(B) * H, uint64_t(kDc + d_r), uint64_t(kDc + d_r), 64))
-    return cudaErrorInvalidValue;
   const dim3 grid(W);
   if (d_r)
     return launch_t<64>(grid, stream, tm_codes, tm_rope, tm_query, q_cat, page_scales, pm, seqlens, B, H,
