@@ -572,24 +572,26 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
       // heads of one 4-column group (512 contiguous bytes), kept in L2 for the
       // combine that reads them next.
       const uint64_t keep = l2_policy_evict_last();
+      // Accumulator column c of product h = c / 128 is latent column
+      // 256 h + 128 pg + c % 128.
+      float* dst = o_part + ((int64_t(slot) * (kDc / 4) + part * 64 + pg * 32) * H + head) * 4;
+      const int64_t step = int64_t(H) * 4;
 #pragma unroll 1
-      for (int c = 128 * part; c < 128 * part + 128; c += 32) {
-        uint32_t r[32];
-        tmem_ld32(lanes + kColO + uint32_t(c), r);
+      for (int c = 0; c < 128; c += 64) {
+        uint32_t r[2][32];
+        tmem_ld32(lanes + kColO + uint32_t(128 * part + c), r[0]);
+        tmem_ld32(lanes + kColO + uint32_t(128 * part + c + 32), r[1]);
         tmem_wait_ld();
-        // Accumulator column c of product h = c / 128 is latent column
-        // 256 h + 128 pg + c % 128.
-        const int col = part * 256 + pg * 128 + c % 128;
-        float* dst = o_part + ((int64_t(slot) * (kDc / 4) + col / 4) * H + head) * 4;
         if (head < H) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            st_global_f4_hint(dst + int64_t(e) * H * 4,
-                              make_float4(__uint_as_float(r[4 * e]) * inv,
-                                          __uint_as_float(r[4 * e + 1]) * inv,
-                                          __uint_as_float(r[4 * e + 2]) * inv,
-                                          __uint_as_float(r[4 * e + 3]) * inv),
-                              keep);
+          for (int e = 0; e < 16; ++e) {
+            const uint32_t* q = r[e / 8] + 4 * (e % 8);
+            st_global_f4_hint(dst, make_float4(__uint_as_float(q[0]) * inv,
+                                               __uint_as_float(q[1]) * inv,
+                                               __uint_as_float(q[2]) * inv,
+                                               __uint_as_float(q[3]) * inv), keep);
+            dst += step;
+          }
         }
       }
       if (pg == 0 && part == 0 && head < H)
