@@ -70,7 +70,8 @@ __device__ __forceinline__ void pair_at(const mla_rope_table& tab, int d_r, int 
 // One warp per token: the row is read once with 16-byte loads and stays in
 // registers (kUnits 16-byte units per lane), the sum of squares is a warp
 // reduction, and the row goes out with 16-byte stores.  Bound by HBM (one read
-// and one write of the row), for a decode step by latency.
+// and one write of the row), for a decode step by latency.  Measured on B200: 8740
+// bf16 tokens 6.3 us (3.2 TB/s of 20 MB; eight warps a block 6.5), 32 tokens 2.5 us.
 constexpr int kWriteWarps = 4;
 
 template <typename T, int kUnits>
@@ -151,7 +152,9 @@ cache_write_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
 // all in flight at once; two blocks share an SM: held in registers, a block
 // filled it and 150 pages took two waves), each warp norms its own, the page's
 // largest magnitude is reduced over the block, the new exponent fixed, and the
-// codes written.  If the page held rows before and its scale grows, those rows
+// codes written.  Measured on B200: 64 tokens, one a page, 4.0 us; 8740 prompt tokens
+// 9.0 us, most of it the arithmetic of the pages (150 of them on 148 SMs: norm, rotate
+// and round 64 rows each).  If the page held rows before and its scale grows, those rows
 // are rescaled first by a power of two, which is exact for the rotary keys and
 // for codes that stay normal E4M3 values and rounds the others once more.
 constexpr int k8Threads = 512;

@@ -9,33 +9,39 @@
 //
 // 8-bit products without widening.  The codes go to the tensor cores as they
 // lie in the cache (kind::f8f6f4, twice the 16-bit rate); what is not 8 bits is
-// split into two E4M3 terms, x = hi + lo, each of 4 significant bits:
-//   * a query row times a power of two (largest value in (224, 448]): a bf16
-//     value has 8 significant bits, so hi + lo is exact for values within 2^10
-//     of the largest, and off by at most 2^-18 of it below;
-//   * a probability: hi is rounded to 4 bits, lo the rest, 2^-8 of p together.
+// split into two terms, x = hi + lo:
+//   * a query row times a power of two (largest value in (224, 448]) into E4M3 +
+//     E4M3: a bf16 value has 8 significant bits and each term holds 4, so hi + lo
+//     is exact for values within 2^10 of the largest, and off by at most 2^-18 of
+//     it below;
+//   * a probability into E4M3 + E5M2: hi is off by at most 2^-4 of p, lo by 2^-3
+//     of that, 2^-7 of p together (1.4e-3 of the output in a simulation of scores
+//     with a deviation of 0.3 to 3.5, as for bf16 probabilities).
 // So both products cost as many tensor cycles as 16-bit ones, but the cache
 // is read, staged and fed at one byte per value and no thread touches it.  The
 // RoPE part is a bf16 product into the same accumulator.
 // The page scale folds into the probability (p_j scale_page enters the second
 // product), so it costs one multiply per key and head group.
 //
-// Range of the probabilities.  E4M3 reaches from 448 to 2^-9, far less than a
-// softmax: with one reference (a running maximum) the keys 2^16 below the
-// largest of the whole sequence would vanish, and thousands of those can carry
-// most of the weight (one early key that outweighs all others).  The reference
-// r therefore follows the tile: it moves when a tile's maximum leaves
-// [r - kFall, r + kRise] (log2), up or down, with O and l rescaled by
-// 2^(r_old - r_new) in fp32; it stays within 2^60 of the largest so far, below
-// which nothing is left to add.  Within a tile of 128 keys values down to
-// 2^-12 of its largest keep a step of at most that largest's 2^-13.
+// Range of the probabilities.  With one reference (a running maximum) keys far
+// below the largest of the whole sequence would vanish in 8 bits, and
+// thousands of those can carry most of the weight (one early key that
+// outweighs all others).  The reference r therefore follows the tile: it moves
+// when a tile's maximum leaves [r - kFall, r + kRise] (log2), up or down, with O
+// and l rescaled by 2^(r_old - r_new) in fp32; it stays within 2^60 of the
+// largest so far, below which nothing is left to add.  A move costs a wait for
+// the last product, so the window is as wide as the two formats allow: E5M2 lo
+// holds what E4M3 hi loses down to 2^-16, so a tile whose maximum lies 2^13
+// below the reference still keeps three bits of keys 2^7 below that.  With E4M3
+// for lo the window was 2^7 wide and two tiles in three moved some row of 128
+// (scores with a deviation of 1.7); now one in forty does.
 //
 // Structure: a cluster of two CTAs (128 heads, 64 each) shares every product
 // with cta_group::2, M = 128.  One CTA alone could not: 128 heads x 512 output
 // columns of fp32 fill its tensor memory, and M = 64 products run at half rate.
 // With the pair each CTA holds its 64 heads' O in 256 columns (an M = 128 pair
 // accumulator keeps columns [0, N/2) in lanes 0-63 and [N/2, N) in lanes
-// 64-127).  Per iteration of two pages (128 keys):
+// 64-127).  Per tile of two pages (128 keys):
 //   S [64 heads each, 128 keys] = Q . K^T: CTA r supplies page r's rows
 //   O [64 heads each, 512] += P . C:     CTA r supplies columns [128 r, +128) and
 //                                        [256 + 128 r, +128) of both pages
@@ -45,13 +51,27 @@
 // same offsets in both CTAs.
 //   warps 0-7  softmax: thread = (head row, page, half of the page's keys);
 //              query split, epilogue
-//   warp 8     K loads (TMA) and page scales;  warp 10  V loads
+//   warp 8     K loads (TMA);  warp 10  V loads
 //   warp 9     QK^T products (leader); in the other CTA it tells the leader that
 //              a K stage has landed
-//   warp 11    P.C products (leader); the same for V
+//   warp 11    P.C products (leader); the same for V.  Two issuing warps: a
+//              product's issue blocks while the tensor pipe is busy, and the waits
+//              before one are hidden behind the other's products
 // The softmax loop is kept short: with 64 keys a thread, unrolled, its code
 // overran the instruction cache and a tile took 5300 cycles, most of them
-// waiting for instructions.
+// waiting for instructions.  Arrivals on the other CTA's barriers have CTA scope
+// (see mbar_arrive_cluster): at cluster scope a tile took 900 cycles more.
+//
+// Measured on B200, 32 x 8192 tokens, 128 heads (decode alone, graphs of ten): 66
+// us, 79 us when repeated without a pause (the clock drops: the products draw
+// the power).  A tile takes 2565 cycles; its products alone 2272 (36 of 33.4
+// cycles and 16 of 67, by a microbenchmark), its shared-memory traffic 2600 at 128
+// bytes a cycle.  About 16,000 cycles go by before the first scores (setup, the
+// query block's copy and split), 4,000 in an epilogue.  Memory would allow 26 us,
+// the bf16 kernel over a bf16 cache takes 92, the fp16-widening 8-bit kernel 128.
+// Tried and not faster: Q hi from tensor memory (less shared-memory traffic,
+// 68.6 us), softmax groups that take tiles in turn (71.0), other orders of the
+// products' terms.
 // Every wait is bounded (about 2 s of SM cycles); on give-up a CTA raises the
 // abort flag of both, records MLA_ERR_DEVICE_TIMEOUT, drains its own loads and
 // products and exits.
@@ -63,7 +83,7 @@ namespace {
 
 using namespace decode8;
 
-constexpr int kKStages = 2, kVStages = 3;   // V: and P, page by page
+constexpr int kKStages = 2, kVStages = 3;   // V, and the pages' P tiles
 constexpr int kKBytes = 5 * kChunk;       // 4 chunks of codes, 1 of RoPE keys
 constexpr int kVBytes = 2 * kChunk;
 constexpr int kSoftmaxWarps = 8;

@@ -5,10 +5,15 @@
 // those of the CTA-pair kernel (k_decode_fp8_paged.cu).  With at most 64 heads
 // half of a pair's rows would be padding and its tile would be staged by two
 // CTAs; here every SM takes tiles of its own.  An M = 64 product runs at half
-// rate, so a 64-key tile costs as many tensor cycles per SM as a pair's 128 keys
-// cost each of its two SMs, but half the rows, loads and power: 64 ragged
-// sequences of up to 32768 tokens measured 222 us with pairs, at 1.5 GHz under
-// the power the padded products took.
+// rate, so a 64-key tile costs as many tensor cycles per SM (36 scores' products
+// of 33 cycles, 8 of P.C of 129: 2220) as a pair's 128 keys cost each of its two
+// SMs, but half the loads and less power, so a higher clock.
+// Measured on B200 (decode alone, graphs of ten): 64 sequences of 512 to 32768
+// tokens with 64 heads 176-181 us, against 222 with pairs; 4 x 4096 tokens with 16
+// heads 11.7 us, against 14.4.  A tile takes 2490 cycles at 1.8 GHz (memory would
+// allow 1750), so the tensor pipe bounds long sequences; a short one is bound by
+// its start, about 9 us from the lengths to the first partial.  Tried and not
+// faster: a fourth stage in the memory of the staged query (182 us).
 //
 // Structure (224 threads):
 //   warp 4     TMA producer: per 64-key page 4 boxes of codes [64 keys x 128] and
@@ -281,7 +286,7 @@ decode8_64_kernel(const __grid_constant__ CUtensorMap tm_codes,
       const int k = query_exponent(top);
       const __nv_bfloat162 inv = __float2bfloat162_rn(exp2i(-k));
       row_factor = exp2i(k);
-#pragma unroll 2
+#pragma unroll 4
       for (int j = 0; j < 16; ++j) {
         const uint4 a = unit(4 * j + 2 * half), b = unit(4 * j + 2 * half + 1);
         const uint32_t wd[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};

@@ -7,7 +7,9 @@
 // Bound by HBM (one read and one write of the rows); small calls by latency.
 // A thread moves 8 pairs with 16-byte accesses and issues its loads before the
 // cosines and sines are formed, once per (token, pair) of the block, in shared
-// memory: with 128 heads that is one sincospif per 64 rotated pairs.
+// memory: with 128 heads that is one sincospif per 128 rotated pairs.  Measured on
+// B200: 4096 tokens x 128 heads x 64 bf16 21.4 us (6.3 TB/s, 0.96 of a copy; 25.9
+// with one row per thread); 64 x 64 rows 2.2 us, 1023 x 16 fp32 rows 3.3 us.
 #include "kernels.h"
 #include "rope_table.cuh"
 
