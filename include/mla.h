@@ -326,7 +326,8 @@ MLA_API int mla_cache_append_paged(const mla_dims* dims, int32_t hidden, const v
  * (angles are exact fractions of a turn at any position).  In place (y = x,
  * same strides) is allowed, other overlaps are not.  dtype MLA_BF16 or
  * MLA_F32; x and y need only their element's alignment (16-byte aligned rows
- * with d_r % 16 == 0 are faster); rows of y must not overlap.
+ * with d_r % 16 == 0 are faster); the rows of y must not overlap, and one of its
+ * two dimensions must lie within the other's stride.
  * mla_rope_init: MLA_ERR_INVALID_ARG for an odd d_r or one outside [2, 256], an
  * unknown layout or scaling, base <= 1, factor < 1, or for YaRN original_len
  * <= 0 or betas that are not beta_fast > beta_slow > 0. */
@@ -436,7 +437,7 @@ MLA_API int mla_cache_write_paged(const mla_dims* dims, int32_t T, const void* x
  * for k^R and for codes that stay normal E4M3 numbers, the others are rounded to
  * nearest even once more).  Rows behind a sequence's last and pages without new
  * tokens stay as they are.  No page may be written for two requests in one
- * call.  A request whose lengths do not fit (negative counts, more than T rows,
+ * call.  query_start ascends.  A request whose lengths do not fit (negative counts, more than T rows,
  * seqlens[b] below its count or above cache_capacity) is skipped, a page id
  * outside the pool skips that page; both record MLA_ERR_BOUNDS.
  * mla_decode_fp8_paged is mla_decode_paged over the dequantised rows [c~ || k^R]:

@@ -683,7 +683,8 @@ def cache_write_paged(dims: Dims, x, gamma, positions, slots, cache_pool, table=
     """mla_cache_write_paged: the rows [RMSNorm(x_c) * gamma || RoPE(x_r, position)] of
     projected tokens x [T, d_c + d_r] to rows ``slots`` (int64, -1: none) of
     cache_pool [num_pages, 64, d_c + d_r].  Without a table x_r is stored as it is."""
-    if _calls is not None and stream is None:
+    if (_calls is not None and stream is None
+            and (table is None or isinstance(table, RopeTable))):
         st = _calls.cache_write_paged(dims.address, x, gamma, positions, slots, cache_pool, table,
                                       eps)
         if st is not None:
@@ -705,7 +706,8 @@ def cache_write_fp8_paged(dims: Dims, x, gamma, query_start, seqlens, block_tabl
     [num_pages, 64, d_c + 2 d_r] uint8 with one scale per page [num_pages];
     request b's rows are x[query_start[b]:query_start[b+1]], the last of its
     seqlens[b] tokens (the lengths after the step)."""
-    if _calls is not None and stream is None:
+    if (_calls is not None and stream is None
+            and (table is None or isinstance(table, RopeTable))):
         st = _calls.cache_write_fp8_paged(dims.address, x, gamma, query_start, seqlens, block_table,
                                           cache_pool, page_scales, table, eps)
         if st is not None:

@@ -200,7 +200,8 @@ cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
   pdl_wait();
 
   // The request whose pages cover this block's index: requests are counted
-  // blockDim at a time, until the one that passes it.
+  // blockDim at a time, until the one that passes it (the last block looks at
+  // all of them, so that lengths that do not fit are always reported).
   int base = 0;
   const int task = blockIdx.x;
   if (tid == 0) s_req = -1;
@@ -232,7 +233,7 @@ cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
     if (task < e && task >= e - n) s_req = b, s_first = e - n;
     if (tid == k8Threads - 1) s_total = e;
     __syncthreads();
-    if (s_req >= 0) break;
+    if (s_req >= 0 && task + 1 < int(gridDim.x)) break;
     base = s_total;
   }
   const int b = s_req;

@@ -459,6 +459,17 @@ bool good_table(const mla_rope_table* t) {
   return t->d_r >= 2 && t->d_r <= 256 && t->d_r % 2 == 0 &&
          (t->layout == MLA_ROPE_HALF || t->layout == MLA_ROPE_INTERLEAVED);
 }
+// Whether n1 x n2 rows of `width` values at these strides are apart, one dimension
+// nested in the other (rows that overlap would be written twice).
+bool rows_apart(int64_t n1, int64_t stride1, int64_t n2, int64_t stride2, int64_t width) {
+  __int128 s1 = stride1 < 0 ? -__int128(stride1) : stride1;
+  __int128 s2 = stride2 < 0 ? -__int128(stride2) : stride2;
+  if (n1 == 1) return n2 == 1 || s2 >= width;
+  if (n2 == 1) return s1 >= width;
+  const bool first_inner = s1 < s2;
+  const __int128 inner = first_inner ? s1 : s2, outer = first_inner ? s2 : s1;
+  return inner >= width && outer >= inner * ((first_inner ? n1 : n2) - 1) + width;
+}
 inline bool aligned_to(const void* p, size_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
@@ -474,10 +485,8 @@ int mla_rope(int32_t dtype, const mla_rope_table* table, int64_t n_tokens, int32
   if (n_tokens >= (int64_t(1) << 31) || H > 65535) return MLA_ERR_UNSUPPORTED;
   if (n_tokens == 0) return MLA_OK;
   if (!x || !y || !pos) return MLA_ERR_INVALID_ARG;
-  // Rows of y that overlap would be written twice.
-  const int64_t d = table->d_r, yt = y_token_stride < 0 ? -y_token_stride : y_token_stride,
-                yh = y_head_stride < 0 ? -y_head_stride : y_head_stride;
-  if ((n_tokens > 1 && yt < d) || (H > 1 && yh < d)) return MLA_ERR_INVALID_ARG;
+  if (!rows_apart(n_tokens, y_token_stride, H, y_head_stride, table->d_r))
+    return MLA_ERR_INVALID_ARG;
   const size_t elem = dtype == MLA_BF16 ? 2 : 4;
   if (!aligned_to(x, elem) || !aligned_to(y, elem) || !aligned_to(pos, 4)) return MLA_ERR_ALIGNMENT;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

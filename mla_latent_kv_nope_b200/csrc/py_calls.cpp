@@ -146,6 +146,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t T = x->size(0), H = nd == 3 ? x->size(1) : 1;
   const void* pos = c.arg(a[2], ScalarType::Int, {T});
   const int transpose = PyObject_IsTrue(a[4]);
+  if (transpose < 0) PyErr_Clear();
   MLA_SLOW_UNLESS(c.ok && transpose >= 0 && H > 0 && c.fits32(H));
   return status(f_rope(type == ScalarType::BFloat16 ? MLA_BF16 : MLA_F32, tab, T, int32_t(H),
                        x->data_ptr(), x->stride(0), nd == 3 ? x->stride(1) : 0,

@@ -200,3 +200,39 @@ def test_host_tensors_are_refused(name, monkeypatch):
     monkeypatch.setattr(bd, "load_library", no_lib)
     with pytest.raises(ValueError, match="CUDA"):
         HOST[name]()
+
+
+@pytest.mark.parametrize("T,H,yt,yh,ok", [
+    (4, 2, 128, 64, True), (4, 2, 64, 256, True), (4, 2, 64, 64, False), (4, 2, 192, 128, True),
+    (4, 2, 96, 64, False), (4, 2, 64, 192, False), (1, 2, 0, 64, True), (4, 1, 64, 0, True),
+    (4, 1, 63, 0, False), (4, 2, -128, 64, True), (4, 2, -64, 64, False),
+    (2, 2, 1 << 62, 1 << 61, True), (3, 3, 1 << 62, 1 << 62, False)])
+def test_rope_refuses_rows_of_y_that_overlap(lib, T, H, yt, yh, ok):
+    """Rows that would be written twice; calls that pass reach the launch, which fails
+    without a GPU (the addresses are never used)."""
+    if ok and torch.cuda.is_available():
+        pytest.skip("a valid call with addresses that do not exist: only without a GPU")
+    tab = mla.rope_table(64)
+    got = lib.mla_rope(bd.MLA_F32, ctypes.byref(tab), T, H, GOOD, 64, 64, GOOD, GOOD, yt, yh, 0, None)
+    assert got == (CUDA if ok else INVALID)
+
+
+def test_paged_cache_counts_rows(monkeypatch):
+    """A step planned for a number of rows is written with that many."""
+    calls = []
+    monkeypatch.setattr(bd, "plan_pages", lambda *a, **kw: calls.append(a[7].shape[0]))
+    monkeypatch.setattr(bd, "cache_write_paged", lambda d, x, g, pos, slots, *a: calls.append(
+        (x.shape[0], pos.shape[0], slots.shape[0])))
+    cache = mla.PagedCache(mla.Dims(2, 16, 512, 64, 128, 128, 128, "bf16"), 4, 16, device="cpu")
+    new = torch.ones(2, dtype=torch.int32)
+    cache.plan(new, tokens=2)
+    cache.write(torch.zeros(2, 576))
+    for n in (1, 3):
+        with pytest.raises(ValueError, match="planned for 2"):
+            cache.write(torch.zeros(n, 576))
+    cache.plan(new)
+    cache.write(torch.zeros(3, 576))
+    assert calls == [2, (2, 2, 2), 16, (3, 3, 3)]
+    for n in (-1, 17):
+        with pytest.raises(ValueError, match="tokens"):
+            cache.plan(new, tokens=n)

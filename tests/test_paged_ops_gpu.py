@@ -6,6 +6,7 @@ Tolerances count roundings: a bf16 result is off by at most 2^-8 of its value,
 an E4M3 code by 2^-4 of its own (2^-10 absolute below 2^-6), plus the fp32
 arithmetic before it, bounded by 2^-20 of the terms' magnitudes (fewer than 16
 roundings of 2^-24, with the angle's 2^-23 and sincospi's 2^-22)."""
+import ctypes
 import math
 import random
 
@@ -919,3 +920,42 @@ def test_paged_serving_run():
         q = feed([1, 1, 0 if i == 1 else 1], 30 + i)
         g.replay()
         check(q)
+
+
+def test_cache_write_fp8_paged_reports_a_bad_length_behind_many_requests():
+    """More requests than a block looks at together, a page for each row of x, and a
+    length that does not fit behind them: reported, the others written."""
+    B, n = 1100, 600
+    dims = mla.Dims(B, 16, 512, 64, 128, 128, PAGE, "bf16")
+    new = [1] * n + [0] * (B - n)
+    qs = np.concatenate([[0], np.cumsum(new)])
+    qs[B] = n + 1                       # the last request claims a row that x does not have
+    lens = [v for v in new[:-1]] + [1]
+    x = randn(1, n, 576, dtype=torch.bfloat16)
+    pool = torch.zeros(B, PAGE, 640, dtype=torch.uint8, device="cuda")
+    sc = torch.full((B,), -1.0, device="cuda")
+    table = i32(np.arange(B)[:, None])
+    mla.cache_write_fp8_paged(dims, x, None, i32(qs), i32(lens), table, pool, sc)
+    torch.cuda.synchronize()
+    assert mla.get_device_status() == 7
+    assert bool((sc[:n] > 0).all()) and bool((sc[n:] == -1).all())
+    assert bool(pool[:n, 0].any(-1).all()) and not pool[n:].any() and not pool[:, 1:].any()
+
+
+def test_tables_that_are_none_are_refused():
+    """Whatever has a rope table's size is not one; neither is an odd truth value."""
+    dims = mla.Dims(1, 16, 512, 64, 128, 128, PAGE, "bf16")
+    x, pool = randn(1, 1, 576, dtype=torch.bfloat16), torch.zeros(1, PAGE, 576, dtype=torch.bfloat16,
+                                                                    device="cuda")
+    fake = np.zeros(ctypes.sizeof(type(mla.rope_table(64))), np.uint8)
+    with pytest.raises(TypeError, match="rope_table"):
+        mla.cache_write_paged(dims, x, None, i32([0]), torch.zeros(1, dtype=torch.int64, device="cuda"),
+                              pool, fake)
+    with pytest.raises(TypeError, match="rope_table"):
+        mla.cache_write_fp8_paged(dims, x, None, i32([0, 1]), i32([1]), i32([[0]]),
+                                  torch.zeros(1, PAGE, 640, dtype=torch.uint8, device="cuda"),
+                                  torch.ones(1, device="cuda"), fake)
+    y = randn(2, 4, 64)
+    with pytest.raises((RuntimeError, ValueError)):
+        mla.rope(mla.rope_table(64), y, i32([0, 1, 2, 3]), out=y, transpose=torch.ones(2))
+    assert mla.get_device_status() == 0
