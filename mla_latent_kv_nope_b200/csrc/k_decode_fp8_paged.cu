@@ -114,8 +114,8 @@ constexpr size_t kOffK = kOffP + size_t(kVStages) * kChunk;
 constexpr size_t kOffV = kOffK + size_t(kKStages) * kKBytes;
 constexpr size_t kOffBars = kOffV + size_t(kVStages) * kVBytes;
 constexpr size_t kOffMax = kOffBars + (sizeof(Bars) + 15) / 16 * 16;   // [2][4][64] floats
-constexpr size_t kOffRowScale = kOffMax + 2 * 4 * 64 * sizeof(float);  // [64] floats
-constexpr size_t kSmemBytes = kOffRowScale + 64 * sizeof(float);
+constexpr size_t kOffRowScale = kOffMax + 2 * 4 * 64 * sizeof(float);  // [2][64] floats
+constexpr size_t kSmemBytes = kOffRowScale + 2 * 64 * sizeof(float);
 static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA");
 
 __device__ __forceinline__ void raise_abort(Bars* bars, int* status) {
@@ -382,6 +382,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
     // heads are another's, or zeros past the end: not stored) is copied as bf16
     // into the shared memory that its E4M3 terms will take, and split in place: a
     // warp takes 8 rows, two at a time, and has read a row before it writes it.
+    // The rows' factors alternate between two buffers: a warp may get here before
+    // another has read the last sequence's.
     uint32_t n_query = 0;
     auto write_query = [&](int b) {
       if (tid == 0 && ok) {
@@ -392,6 +394,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
           tma_load_2d(&tm_query, &bars->q_raw, smem + kOffQ + c * kChunk, c * 64,
                       b * H + g * kHeadsPerCta);
       }
+      float* factor = s_row + (n_query & 1) * 64;
       await(&bars->q_raw, n_query++ & 1);
       // 16-byte unit un (8 values) of row qr.
       auto unit = [&](int qr, int un) {
@@ -420,7 +423,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
           top[r] = __reduce_max_sync(0xffffffffu, larger_half(top[r]));
           const int k = query_exponent(top[r]);
           inv[r] = __float2bfloat162_rn(exp2i(-k));
-          if (lane == 0) s_row[8 * warp + r0 + r] = exp2i(k);
+          if (lane == 0) factor[8 * warp + r0 + r] = exp2i(k);
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -466,7 +469,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
         }
       }
       meet_all();                                      // every row's factor is written
-      const float row_scale = s_row[row] * scale_log2;
+      const float row_scale = s_row[((n_query - 1) & 1) * 64 + row] * scale_log2;
       float ref = 0.f, top = -INFINITY, l_sum = 0.f;   // ref: set by the first tile
       for (int64_t t = lo; t < hi; t += 2, ++i) {
         const int sb = i & 1;

@@ -54,7 +54,8 @@ constexpr uint32_t kIdescPV = idesc_f16_f32(64, 256, false, true);
 
 struct Bars {
   uint64_t full[kStages], empty[kStages];
-  uint64_t s_full[2], s_free[2], p_full[2];
+  uint64_t s_full[2], s_free[2];
+  uint64_t p_full[kStages];   // by stage: a warp a tile ahead of another cannot speak for it
   uint64_t q_raw, q_raw_free, q_ready, o_free, qk_drain, pv_drain, never;
   uint32_t tmem_base;
   int abort_flag;
@@ -93,11 +94,14 @@ decode8_64_kernel(const __grid_constant__ CUtensorMap tm_codes,
     prefetch_queries(q_cat, int64_t(B) * H * (kDc + kDr) * 2, w, W);
   const int32_t len0 = int(threadIdx.x) < B ? seqlens[threadIdx.x] : 0;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&bars->full[s], 1), mbar_init(&bars->empty[s], 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
+      mbar_init(&bars->p_full[s], kSoftmaxWarps);
+    }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->s_full[s], 1);
       mbar_init(&bars->s_free[s], kSoftmaxWarps);
-      mbar_init(&bars->p_full[s], kSoftmaxWarps);
     }
     mbar_init(&bars->q_raw, 1);
     mbar_init(&bars->q_raw_free, kSoftmaxWarps);
@@ -227,7 +231,7 @@ decode8_64_kernel(const __grid_constant__ CUtensorMap tm_codes,
         // The previous sequence's epilogue has read O before it is overwritten.
         if (t == seg.lo && n_seg > 0 && !(ok = wait_w(&bars->o_free, (n_seg - 1) & 1, abort_flag)))
           break;
-        if (!(ok = wait_w(&bars->p_full[i & 1], (i >> 1) & 1, abort_flag))) break;
+        if (!(ok = wait_w(&bars->p_full[st], (i / kStages) & 1, abort_flag))) break;
         tc_fence_after();
         const uint64_t off = uint64_t((uint32_t(st) * kStageBytes) >> 4);
 #pragma unroll
@@ -399,7 +403,7 @@ decode8_64_kernel(const __grid_constant__ CUtensorMap tm_codes,
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        arrive(&bars->p_full[sb]);
+        arrive(&bars->p_full[st]);
       }
       if (!ok) break;
       // Every QK^T of this sequence has been read back: load the next query.
