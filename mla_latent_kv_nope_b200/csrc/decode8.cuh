@@ -108,7 +108,12 @@ __device__ __forceinline__ bool find_segments(int32_t len0, const int32_t* seqle
 #pragma unroll
   for (int k = 0; k < kWarps; ++k) total += scratch[k];
   __syncthreads();
-  const int64_t u0 = worker_tile_begin(w, total, W), u1 = worker_tile_begin(w + 1, total, W);
+  // (A 64-bit division is a long subroutine; both are needed at once here.)
+  const bool small = total * W <= int64_t(UINT32_MAX);
+  const int64_t u0 = small ? int64_t(uint32_t(w) * uint32_t(total) / uint32_t(W))
+                           : worker_tile_begin(w, total, W);
+  const int64_t u1 = small ? int64_t(uint32_t(w + 1) * uint32_t(total) / uint32_t(W))
+                           : worker_tile_begin(w + 1, total, W);
   if (u0 >= u1) return false;
   // The sequence that unit u0 belongs to, kThreads of them at a time.
   int64_t base = 0;
@@ -234,6 +239,15 @@ __device__ __forceinline__ void prefetch_queries(const __nv_bfloat16* q_cat, int
   const int64_t at = cta * share, end = min(at + share, bytes);
   if (at < end)
     bulk_prefetch_l2(reinterpret_cast<const char*>(q_cat) + at, uint32_t(end - at));
+}
+
+// The block table into L2 while the lengths are on their way (one warp: at most a
+// line a lane, so the first 600 KB of a larger table).
+__device__ __forceinline__ void prefetch_table(const PageMap& pm, int B, int64_t cta,
+                                               int64_t n_cta) {
+  const int64_t line = (threadIdx.x & 31) * n_cta + cta;
+  if (line * 128 < int64_t(B) * pm.max_blocks * 4)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(pm.table) + line * 128));
 }
 
 // Page rows and scales of a run of tiles: lane l holds tile base + l, and the

@@ -141,12 +141,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
   const int g = blockIdx.x, w = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  pdl_wait();
-  // Asked for before the setup that it does not depend on.
-  if (threadIdx.x == 32 * kKWarp)
-    prefetch_queries(q_cat, int64_t(B) * H * R * 2, int64_t(blockIdx.y) * gridDim.x + blockIdx.x,
-                     int64_t(gridDim.x) * gridDim.y);
-  const int32_t len0 = int(threadIdx.x) < B ? seqlens[threadIdx.x] : 0;
+  // What reads nothing of earlier kernels comes before the wait for them, the
+  // meeting with the other CTA too (after it, it would wait for the loads below).
   if (threadIdx.x == 0) {
     // The leader's also wait for the other CTA's word that its stage has landed.
     const uint32_t n_full = rank == 0 ? 2 : 1;
@@ -168,25 +164,30 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (warp == kQkWarp) {
-    tmem_alloc_pair(&bars->tmem_base, kTmemCols);
-    tmem_relinquish_pair();
-  }
   if (threadIdx.x == 32 * kKWarp) {
     tma_prefetch_desc(&tm_codes);
     tma_prefetch_desc(&tm_query);
     if (kDr) tma_prefetch_desc(&tm_rope);
   }
-  tc_fence_before();
-  __syncthreads();
   cluster_sync();
+  pdl_wait();
+  const int32_t len0 = int(threadIdx.x) < B ? seqlens[threadIdx.x] : 0;
+  if (warp == kQkWarp) {
+    tmem_alloc_pair(&bars->tmem_base, kTmemCols);
+    tmem_relinquish_pair();
+  } else if (warp == kVWarp) {
+    const int64_t cta = int64_t(blockIdx.y) * gridDim.x + blockIdx.x,
+                  n_cta = int64_t(gridDim.x) * gridDim.y;
+    if (lane == 0) prefetch_queries(q_cat, int64_t(B) * H * R * 2, cta, n_cta);
+    prefetch_table(pm, B, cta, n_cta);
+  }
+  tc_fence_before();
+  Segments seg;       // (its barriers also make tmem_base visible)
+  const bool busy = find_segments<kThreads>(len0, seqlens, B, cap, w, W,
+                                            reinterpret_cast<int64_t*>(smem), &seg);
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort_flag;
-
-  Segments seg;
-  const bool busy = find_segments<kThreads>(len0, seqlens, B, cap, w, W,
-                                            reinterpret_cast<int64_t*>(smem), &seg);
   uint32_t n_issued = 0;     // K or V stages that this producer warp has loaded into
   bool ok = true;
 
@@ -384,16 +385,17 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
     // warp takes 8 rows, two at a time, and has read a row before it writes it.
     // The rows' factors alternate between two buffers: a warp may get here before
     // another has read the last sequence's.
-    uint32_t n_query = 0;
-    auto write_query = [&](int b) {
-      if (tid == 0 && ok) {
-        fence_proxy_async_smem();   // after what threads have read and written there
-        mbar_arrive_expect_tx(&bars->q_raw, (R / 64) * kChunk);
+    uint32_t n_query = 0, n_copied = 0;   // query blocks split; copied (by thread 0)
+    auto copy_query = [&](int b) {
+      fence_proxy_async_smem();   // after what threads have read and written there
+      mbar_arrive_expect_tx(&bars->q_raw, (R / 64) * kChunk);
 #pragma unroll 1
-        for (int c = 0; c < R / 64; ++c)
-          tma_load_2d(&tm_query, &bars->q_raw, smem + kOffQ + c * kChunk, c * 64,
-                      b * H + g * kHeadsPerCta);
-      }
+      for (int c = 0; c < R / 64; ++c)
+        tma_load_2d(&tm_query, &bars->q_raw, smem + kOffQ + c * kChunk, c * 64,
+                    b * H + g * kHeadsPerCta);
+      ++n_copied;
+    };
+    auto write_query = [&] {
       float* factor = s_row + (n_query & 1) * 64;
       await(&bars->q_raw, n_query++ & 1);
       // 16-byte unit un (8 values) of row qr.
@@ -455,14 +457,17 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
     };
 
     bool more = seg.next();
-    if (more) write_query(seg.cur);
+    if (more && tid == 0) copy_query(seg.cur);
+    if (more) write_query();
     while (more) {
       const int b = seg.cur;
       const int64_t lo = seg.lo, hi = seg.hi, L = seg.L;
       PageWalk walk(pm, page_scales, b, lo, hi);
-      if (tid == 0) {      // the next sequence's query block into L2 ahead of its use
+      int next_b = -1;     // thread 0: the next sequence; its query block into L2 ahead of its use
+      if (tid == 0) {
         Segments ahead = seg;
         if (ahead.next()) {
+          next_b = ahead.cur;
           const int64_t r0 = int64_t(ahead.cur) * H + g * kHeadsPerCta;
           const int rows = min(H - g * kHeadsPerCta, kHeadsPerCta);
           if (rows > 0) bulk_prefetch_l2(q_cat + r0 * R, uint32_t(rows * R * 2));
@@ -474,6 +479,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
       for (int64_t t = lo; t < hi; t += 2, ++i) {
         const int sb = i & 1;
         await(&bars->s_full[sb], (i >> 1) & 1);
+        // With this sequence's last scores its query block is free.
+        if (next_b >= 0 && t + 2 >= hi && ok) copy_query(next_b);
         tc_fence_after();
         uint32_t x[32];          // keys 32 part .. of the page
         tmem_ld32(lanes + kColS + uint32_t(sb) * 64u + uint32_t(part) * 32u, x);
@@ -576,9 +583,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
         tc_fence_before();
         arrive(sb ? a_p1 : a_p0);
       }
-      // Every QK^T of this sequence has been read back: load the next query.
       more = seg.next();
-      if (more) write_query(seg.cur);
+      if (more) write_query();
       // Epilogue: normalised partial output and log-sum-exp.
       // The four parts' sums meet in the buffer that the last tile did not use
       // (some warp may still be reading the other; the next sequence's first
@@ -622,9 +628,9 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
       tc_fence_before();
       arrive(a_o);
     }
-    if (tid == 0 && n_query) {   // the last copy has landed, after a give-up as well
+    if (tid == 0 && n_copied) {   // the last copy has landed, after a give-up as well
       volatile int no_abort = 0;
-      mbar_wait(&bars->q_raw, (n_query - 1) & 1, &no_abort, kWaitLimitCycles / 100);
+      mbar_wait(&bars->q_raw, (n_copied - 1) & 1, &no_abort, kWaitLimitCycles / 100);
     }
   }
   if (!ok && lane == 0) raise_abort(bars, status);

@@ -88,11 +88,7 @@ decode8_64_kernel(const __grid_constant__ CUtensorMap tm_codes,
   const int w = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  pdl_wait();
-  // Asked for before the setup that it does not depend on.
-  if (threadIdx.x == 32 * kProducerWarp)
-    prefetch_queries(q_cat, int64_t(B) * H * (kDc + kDr) * 2, w, W);
-  const int32_t len0 = int(threadIdx.x) < B ? seqlens[threadIdx.x] : 0;
+  // What reads nothing of earlier kernels comes before the wait for them.
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars->full[s], 1);
@@ -114,23 +110,27 @@ decode8_64_kernel(const __grid_constant__ CUtensorMap tm_codes,
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (warp == kQkWarp) {
-    tmem_alloc(&bars->tmem_base, kTmemCols);
-    tmem_relinquish();
-  }
   if (threadIdx.x == 32 * kProducerWarp) {
     tma_prefetch_desc(&tm_codes);
     tma_prefetch_desc(&tm_query);
     if (kDr) tma_prefetch_desc(&tm_rope);
   }
+  pdl_wait();
+  const int32_t len0 = int(threadIdx.x) < B ? seqlens[threadIdx.x] : 0;
+  if (warp == kQkWarp) {
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    tmem_relinquish();
+  } else if (warp == kProducerWarp) {
+    if (lane == 0) prefetch_queries(q_cat, int64_t(B) * H * (kDc + kDr) * 2, w, W);
+    prefetch_table(pm, B, w, W);
+  }
   tc_fence_before();
-  __syncthreads();
+  Segments seg;       // (its barriers also make tmem_base and the barriers visible)
+  const bool busy = find_segments<kThreads>(
+      len0, seqlens, B, cap, w, W, reinterpret_cast<int64_t*>(smem + kOffScratch), &seg);
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort_flag;
-  Segments seg;
-  const bool busy = find_segments<kThreads>(
-      len0, seqlens, B, cap, w, W, reinterpret_cast<int64_t*>(smem + kOffScratch), &seg);
   uint32_t n_issued = 0, n_queries = 0;   // tiles and query blocks the producer has asked for
   bool ok = true;
 
