@@ -62,11 +62,11 @@
 // waiting for instructions.  Arrivals on the other CTA's barriers have CTA scope
 // (see mbar_arrive_cluster): at cluster scope a tile took 900 cycles more.
 //
-// Measured on B200, 32 x 8192 tokens, 128 heads (decode alone, graphs of ten): 66
+// Measured on B200, 32 x 8192 tokens, 128 heads (decode alone, graphs of ten): 64.5
 // us, 79 us when repeated without a pause (the clock drops: the products draw
 // the power).  A tile takes 2565 cycles; its products alone 2272 (36 of 33.4
 // cycles and 16 of 67, by a microbenchmark), its shared-memory traffic 2600 at 128
-// bytes a cycle.  About 16,000 cycles go by before the first scores (setup, the
+// bytes a cycle.  About 14,000 cycles go by before the first scores (setup, the
 // query block's copy and split), 4,000 in an epilogue.  Memory would allow 26 us,
 // the bf16 kernel over a bf16 cache takes 92, the fp16-widening 8-bit kernel 128.
 // Tried and not faster: Q hi from tensor memory (less shared-memory traffic,

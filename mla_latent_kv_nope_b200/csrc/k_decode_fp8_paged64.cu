@@ -13,7 +13,8 @@
 // heads 11.7 us, against 14.4.  A tile takes 2490 cycles at 1.8 GHz (memory would
 // allow 1750), so the tensor pipe bounds long sequences; a short one is bound by
 // its start, about 9 us from the lengths to the first partial.  Tried and not
-// faster: a fourth stage in the memory of the staged query (182 us).
+// faster: a fourth stage in the memory of the staged query (182 us), four more warps
+// for the query split and the epilogue (11.8 against 12.1 us, then no difference).
 //
 // Structure (224 threads):
 //   warp 4     TMA producer: per 64-key page 4 boxes of codes [64 keys x 128] and
