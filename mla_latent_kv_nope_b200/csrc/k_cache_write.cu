@@ -6,6 +6,7 @@
 
 #include "kernels.h"
 #include "rope_table.cuh"
+#include "sm100.cuh"
 
 namespace mla {
 
@@ -146,19 +147,17 @@ cache_write_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
 }
 
 // ---------------------------------------------------------------- 8-bit pages
-// One block per (request, page that its new tokens touch), at most 64 rows.
-// Bound by latency (a decode step; a page per SM for prompts of some thousand
-// tokens).  The rows are copied to shared memory asynchronously (one read of x,
-// all in flight at once; two blocks share an SM: held in registers, a block
-// filled it and 150 pages took two waves), each warp norms its own, the page's
-// largest magnitude is reduced over the block, the new exponent fixed, and the
-// codes written.  Measured on B200: 64 tokens, one a page, 4.0 us; 8740 prompt tokens
-// 9.0 us, most of it the arithmetic of the pages (150 of them on 148 SMs: norm, rotate
-// and round 64 rows each).  If the page held rows before and its scale grows, those rows
-// are rescaled first by a power of two, which is exact for the rotary keys and
-// for codes that stay normal E4M3 values and rounds the others once more.
-constexpr int k8Threads = 512;
-constexpr int k8Warps = k8Threads / 32;
+// One block, or a cluster of two or four that share the rows, per (request, page that
+// its new tokens touch).  Bound by latency: the lengths, the page id and the rows, the
+// page's maximum, and the arithmetic of a page's rows on one SM, which is why the page
+// is shared.  The rows are copied to shared memory asynchronously (one read of x, all
+// in flight at once; held in registers, a block filled an SM and 150 pages took two
+// waves), each warp norms its own, the page's largest magnitude is reduced over the
+// block and the cluster, the new exponent fixed, and the codes written.  Measured on
+// B200: 64 tokens, one a page, 4.0 us; 8740 prompt tokens 8.0 us (9.2 with one block a
+// page), 1000 tokens of one prompt 4.9 us (6.8).  If the page held rows before and its
+// scale grows, those rows are rescaled first by a power of two, which is exact for the
+// rotary keys and for codes that stay normal E4M3 values and rounds the others once more.
 constexpr int k8Dc = 512;
 constexpr int kMinScaleExp = -40, kMaxScaleExp = 120;
 
@@ -183,27 +182,38 @@ __device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float f) {
                 __high2float(hi) * f);
 }
 
-template <int kDr>
-__global__ void __launch_bounds__(k8Threads, 2)
+template <int kDr, int kSplit>
+struct Write8 {
+  static constexpr int kRows = kTileKeys / kSplit;             // of a page, a block's
+  static constexpr int kThreads = kSplit == 1 ? 512 : 256;
+  static constexpr size_t kSmem = size_t(kRows) * 2 * (k8Dc + kDr);
+};
+
+template <int kDr, int kSplit>
+__global__ void __launch_bounds__(Write8<kDr, kSplit>::kThreads, kSplit == 1 ? 2 : 4)
 cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
                     const __nv_bfloat16* __restrict__ x, int64_t x_stride, int T_rows,
                     const float* __restrict__ gamma, float eps,
                     const int32_t* __restrict__ query_start, const int32_t* __restrict__ seqlens,
                     int B, int64_t cap, const PageMap pm, uint8_t* __restrict__ pool,
                     float* __restrict__ page_scales, int* __restrict__ status) {
-  constexpr int kRowBytes = k8Dc + 2 * kDr;
-  extern __shared__ __align__(16) uint8_t s_x[];   // [64 rows][d_c + d_r] bf16 as they came
+  constexpr int kRowBytes = k8Dc + 2 * kDr, kRows = Write8<kDr, kSplit>::kRows;
+  constexpr int k8Threads = Write8<kDr, kSplit>::kThreads, k8Warps = k8Threads / 32;
+  extern __shared__ __align__(16) uint8_t s_x[];   // [kRows][d_c + d_r] bf16 as they came
   __shared__ int s_scan[k8Warps];
   __shared__ int s_req, s_first, s_total;
-  __shared__ float s_max[k8Warps], s_inv[kTileKeys];
+  __shared__ float s_max[k8Warps], s_inv[kRows];
+  __shared__ float s_peer[kSplit];                 // each block's largest magnitude
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = kSplit > 1 ? int(sm100::cluster_rank()) : 0;
+  if (kSplit > 1) sm100::cluster_sync();           // all have started: their shared memory is there
   pdl_wait();
 
   // The request whose pages cover this block's index: requests are counted
   // blockDim at a time, until the one that passes it (the last block looks at
   // all of them, so that lengths that do not fit are always reported).
   int base = 0;
-  const int task = blockIdx.x;
+  const int task = blockIdx.x / kSplit, tasks = int(gridDim.x) / kSplit;
   if (tid == 0) s_req = -1;
   __syncthreads();
   for (int b0 = 0; b0 < B; b0 += k8Threads) {
@@ -233,7 +243,7 @@ cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
     if (task < e && task >= e - n) s_req = b, s_first = e - n;
     if (tid == k8Threads - 1) s_total = e;
     __syncthreads();
-    if (s_req >= 0 && task + 1 < int(gridDim.x)) break;
+    if (s_req >= 0 && task + 1 < tasks) break;
     base = s_total;
   }
   const int b = s_req;
@@ -244,15 +254,17 @@ cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
   const int r0 = int(max(start - j * kTileKeys, int64_t(0)));                    // new rows
   const int r1 = int(min(end - j * kTileKeys, int64_t(kTileKeys)));              // [r0, r1)
   const int64_t x0 = q0 + j * kTileKeys - start;                                 // x row of page row 0
+  // This block's rows of the page: [p0, p1), new ones [n0, n1).
+  const int p0 = rank * kRows, p1 = p0 + kRows, n0 = max(r0, p0), n1 = min(r1, p1);
   // The page id and x are asked for together.
   const int64_t first = pm.tile_row(b, j);
 
-  // Rows r0 + warp, r0 + warp + 16, ... of the page are this warp's.
+  // Every k8Warps-th new row is this warp's.
   constexpr int kXBytes = 2 * (k8Dc + kDr);
 #pragma unroll 1
-  for (int r = r0 + warp; r < r1; r += k8Warps) {
+  for (int r = n0 + warp; r < n1; r += k8Warps) {
     const char* src = reinterpret_cast<const char*>(x + (x0 + r) * x_stride);
-    const uint32_t dst = uint32_t(__cvta_generic_to_shared(s_x + r * kXBytes));
+    const uint32_t dst = uint32_t(__cvta_generic_to_shared(s_x + (r - p0) * kXBytes));
 #pragma unroll
     for (int u = lane; u < kXBytes / 16; u += 32)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + u * 16), "l"(src + u * 16)
@@ -272,7 +284,7 @@ cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
   auto row_values = [&](int r, float (&f)[16]) {
-    const uint4* row = reinterpret_cast<const uint4*>(s_x + r * kXBytes);
+    const uint4* row = reinterpret_cast<const uint4*>(s_x + (r - p0) * kXBytes);
     unpack16<__nv_bfloat16, 8>(row[lane], *reinterpret_cast<float(*)[8]>(f));
     unpack16<__nv_bfloat16, 8>(row[lane + 32], *reinterpret_cast<float(*)[8]>(f + 8));
   };
@@ -284,7 +296,7 @@ cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
   // its code costs is mostly the fetching of it.
   float amax = 0.f;
 #pragma unroll 1
-  for (int r = r0 + warp; r < r1; r += k8Warps) {
+  for (int r = n0 + warp; r < n1; r += k8Warps) {
     float f[16], ss = 0.f;
     row_values(r, f);
 #pragma unroll
@@ -297,13 +309,21 @@ cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
       top = fmaxf(top, fmaxf(fabsf(f[e]), fabsf(f[e + 1])));
     }
     amax = fmaxf(amax, top * inv);
-    if (lane == 0) s_inv[r] = inv;
+    if (lane == 0) s_inv[r - p0] = inv;
   }
   amax = warp_max(amax);
   if (lane == 0) s_max[warp] = amax;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < k8Warps; ++w) amax = fmaxf(amax, s_max[w]);
+  if constexpr (kSplit > 1) {
+    // Each block tells the others; all have read the page's scale when they meet.
+    if (tid < kSplit)
+      sm100::st_cluster_u32(sm100::cluster_map(&s_peer[rank], uint32_t(tid)), __float_as_uint(amax));
+    sm100::cluster_sync();
+#pragma unroll
+    for (int w = 0; w < kSplit; ++w) amax = fmaxf(amax, s_peer[w]);
+  }
   int k = scale_exponent(amax);
   if (r0 && old_scale > 0.f && old_scale < INFINITY) {
     int e;
@@ -311,7 +331,7 @@ cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
     k = max(k, min(f > 0.5f ? e : e - 1, kMaxScaleExp));
     const float ratio = old_scale * ldexpf(1.f, -k);
     if (ratio != 1.f)
-      for (int r = warp; r < r0; r += k8Warps) {
+      for (int r = p0 + warp; r < min(r0, p1); r += k8Warps) {
         uint4* row = reinterpret_cast<uint4*>(page + r * kRowBytes);
         uint4 c = row[lane];
         c.x = rescale_e4m3x4(c.x, ratio);
@@ -329,10 +349,10 @@ cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
       }
   }
   const float inv_scale = ldexpf(1.f, -k);
-  if (tid == 0) *page_scale = ldexpf(1.f, k);
+  if (tid == 0 && rank == 0) *page_scale = ldexpf(1.f, k);
 #pragma unroll 1
-  for (int r = r0 + warp; r < r1; r += k8Warps) {
-    const float inv = s_inv[r] * inv_scale;   // the power of two commutes with the roundings
+  for (int r = n0 + warp; r < n1; r += k8Warps) {
+    const float inv = s_inv[r - p0] * inv_scale;   // the power of two commutes with the roundings
     uint8_t* row = page + r * kRowBytes;
     float f[16];
     row_values(r, f);
@@ -346,7 +366,7 @@ cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
     reinterpret_cast<uint2*>(row)[lane + 32] =
         make_uint2(e4m3x4(f[8], f[9], f[10], f[11]), e4m3x4(f[12], f[13], f[14], f[15]));
     if constexpr (kDr > 0) {
-      const __nv_bfloat16* xr = reinterpret_cast<const __nv_bfloat16*>(s_x + r * kXBytes) + k8Dc;
+      const __nv_bfloat16* xr = reinterpret_cast<const __nv_bfloat16*>(s_x + (r - p0) * kXBytes) + k8Dc;
       const float a = __bfloat162float(xr[ra]), c = __bfloat162float(xr[rc]);
       float y1 = a, y2 = c;
       if (rotate) {
@@ -397,19 +417,47 @@ cudaError_t launch_cache_write_fp8(const mla_rope_table* tab, const __nv_bfloat1
                                    int64_t x_stride, int T_rows, const float* gamma, float eps,
                                    const int32_t* query_start, const int32_t* seqlens, int B,
                                    int64_t cap, int d_r, const PageMap& pm, uint8_t* pool,
-                                   float* page_scales, int* status, cudaStream_t stream) {
+                                   float* page_scales, int* status, int sms,
+                                   cudaStream_t stream) {
   const mla_rope_table t = tab ? *tab : mla_rope_table{};
   // A request with n new tokens touches at most min(n, n / 64 + 2) pages.
   const int64_t most = int64_t(T_rows) / kTileKeys + 2 * int64_t(B);
-  const dim3 grid(unsigned(most < T_rows ? most : T_rows));
-  auto kernel = d_r ? cache_write8_kernel<64> : cache_write8_kernel<0>;
-  const size_t smem = size_t(kTileKeys) * 2 * (k8Dc + d_r);
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             int(smem));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, grid, dim3(k8Threads), smem, stream, t, int(tab != nullptr), x, x_stride,
-                    T_rows, gamma, eps, query_start, seqlens, B, cap, pm, pool, page_scales,
-                    status);
+  const int64_t tasks = most < T_rows ? most : T_rows;
+  auto go = [&](auto kernel, auto shape) {
+    using S = decltype(shape);
+    const int split = kTileKeys / S::kRows;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(tasks * split));
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(split);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 2 : 1;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               int(S::kSmem));
+    if (e != cudaSuccess) return e;
+    return cudaLaunchKernelEx(&cfg, kernel, t, int(tab != nullptr), x, x_stride, T_rows, gamma, eps,
+                              query_start, seqlens, B, cap, pm, pool, page_scales, status);
+  };
+  // Blocks to a page.  With a row or two a page there is nothing to share (64 pages:
+  // 4.0 us, shared by four blocks 4.5).  Four blocks while all of them run at once: 66
+  // pages 5.7 us against 6.0 with two and 6.9 with one, 103 pages 6.7, 7.0 and 7.0,
+  // but 168 pages 11.3, 8.0 and 9.2.  Beyond that two blocks keep even with one or ahead
+  // (628 pages 22.0 against 23.0, 700 pages of 200 prompts 21.5 against 21.0).
+  if (T_rows <= 2 * int64_t(B))
+    return d_r ? go(cache_write8_kernel<64, 1>, Write8<64, 1>{})
+               : go(cache_write8_kernel<0, 1>, Write8<0, 1>{});
+  if (4 * tasks <= 3 * int64_t(sms))
+    return d_r ? go(cache_write8_kernel<64, 4>, Write8<64, 4>{})
+               : go(cache_write8_kernel<0, 4>, Write8<0, 4>{});
+  return d_r ? go(cache_write8_kernel<64, 2>, Write8<64, 2>{})
+             : go(cache_write8_kernel<0, 2>, Write8<0, 2>{});
 }
 
 }  // namespace mla

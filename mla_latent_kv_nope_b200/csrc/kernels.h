@@ -150,7 +150,8 @@ cudaError_t launch_cache_write_fp8(const mla_rope_table* tab, const __nv_bfloat1
                                    int64_t x_stride, int T_rows, const float* gamma, float eps,
                                    const int32_t* query_start, const int32_t* seqlens, int B,
                                    int64_t cap, int d_r, const PageMap& pm, uint8_t* pool,
-                                   float* page_scales, int* status, cudaStream_t stream);
+                                   float* page_scales, int* status, int sms,
+                                   cudaStream_t stream);
 
 // Decode over a paged 8-bit cache with one scale per page (d_c = 512, d_r = 64
 // or 0), and its default split count on a device of `sms` SMs.

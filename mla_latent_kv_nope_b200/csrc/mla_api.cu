@@ -616,7 +616,7 @@ int mla_cache_write_fp8_paged(const mla_dims* d, int32_t T, const void* x, int64
       table, static_cast<const __nv_bfloat16*>(x), x_stride, T, gamma, eps, query_start, seqlens,
       d->B, d->cache_capacity, d->d_r,
       PageMap{block_table, max_blocks, num_pages, d->cache_capacity},
-      static_cast<uint8_t*>(cache_pool), page_scales, status_ptr(),
+      static_cast<uint8_t*>(cache_pool), page_scales, status_ptr(), sm_count(),
       static_cast<cudaStream_t>(stream)));
 }
 

@@ -487,6 +487,39 @@ def test_cache_write_fp8_paged(ctx, new, d_r, layout, grow):
                 assert torch.equal(mem[p], before[p]) and scales[p].item() == old[2][p]
 
 
+@pytest.mark.parametrize("ctx,new,d_r,grow", [
+    ([40], [7500], 64, 9.0), ([40, 3], [7500, 90], 0, 9.0),    # two blocks to a page
+    ([40], [900], 64, 9.0), ([0, 17, 33], [3, 2, 500], 0, 9.0),   # four
+])
+def test_cache_write_fp8_paged_blocks_that_share_a_page(ctx, new, d_r, grow):
+    """Prompts of several lengths: every block of a page uses the maximum of all its rows and
+    rescales its part of the earlier ones."""
+    B, R, blocks = len(ctx), 512 + d_r, 120
+    lens = [a + n for a, n in zip(ctx, new)]
+    pool = Pool(lens, sum(-(-n // PAGE) for n in lens) + 2, blocks)
+    dims = mla.Dims(B, 16, 512, d_r, 128, 128, blocks * PAGE, "bf16")
+    tab = mla.rope_table(d_r) if d_r else None
+    mem = torch.randint(0, 0x7E, (pool.num_pages, PAGE, 512 + 2 * d_r), dtype=torch.uint8).cuda()
+    if d_r:
+        mem[..., 512:] = randn(8, pool.num_pages, PAGE, d_r, dtype=torch.bfloat16).view(torch.uint8)
+    scales = torch.exp2(torch.randint(-9, -5, (pool.num_pages,)).float()).cuda()
+    gamma = grow * (1 + 0.1 * randn(3, 512))
+    qs = np.concatenate([[0], np.cumsum(new)]).tolist()
+    x = randn(12, qs[-1], R, dtype=torch.bfloat16)
+    # One row in a hundred is far from even, so that a page's maximum lies in one block.
+    x[::100, 7] *= 200
+    old = (codes64(mem), rope_part(mem) if d_r else np.zeros((pool.num_pages, PAGE, 0)), f64(scales))
+    before = mem.clone()
+    ref = write8_64([a.copy() for a in old], f64(x), qs, lens, pool.table, f64(gamma), d_r, "half")
+    mla.cache_write_fp8_paged(dims, x, gamma, i32(qs), i32(lens), pool.d_table, mem, scales, tab)
+    assert mla.get_device_status() == 0
+    check_pages8(mem, scales, *ref)
+    for b in range(B):
+        j = (lens[b] - 1) // PAGE
+        p, end = pool.table[b][j], lens[b] - j * PAGE
+        assert torch.equal(mem[p, end:], before[p, end:])
+
+
 def test_cache_write_fp8_paged_token_by_token():
     """One token at a time gives the page's scale of a whole write, codes within a
     second rounding, and a fresh page ignores what its scale was before."""
