@@ -55,14 +55,6 @@ __device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity, volatile 
   }
 }
 
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
-  const __half2 h(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(c), __NV_E4M3));
-  return __half22float2(h);
-}
-
 // The sequences whose tiles lie in this worker's range of work units (as in
 // tile_deal.cuh, for any batch size): every role walks them by itself from the
 // first one, whose number and unit prefix the block finds together.

@@ -992,3 +992,25 @@ def test_tables_that_are_none_are_refused():
     with pytest.raises((RuntimeError, ValueError)):
         mla.rope(mla.rope_table(64), y, i32([0, 1, 2, 3]), out=y, transpose=torch.ones(2))
     assert mla.get_device_status() == 0
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_paged_cache_step_of_a_stated_size(fp8):
+    """A step planned for fewer rows than its tokens is not begun, and nothing is written."""
+    dims = mla.Dims(2, 16, 512, 64, 128, 128, 128, "bf16")
+    cache = mla.PagedCache(dims, num_pages=4, max_tokens=64, fp8=fp8, table=mla.rope_table(64))
+    x = randn(1, 5, 576, dtype=torch.bfloat16)
+    cache.plan(i32([3, 2]), tokens=4)
+    cache.write(x[:4])
+    assert mla.get_device_status() == 7
+    assert cache.seqlens.tolist() == [0, 0] and cache.free_count.item() == 4
+    assert not cache.pool.any() and bool((cache.block_table == -1).all())
+    cache.plan(i32([3, 2]), tokens=5)
+    cache.write(x)
+    assert mla.get_device_status() == 0 and cache.seqlens.tolist() == [3, 2]
+    cache.plan(i32([1, 0]), tokens=1)
+    cache.write(x[:1])
+    assert mla.get_device_status() == 0 and cache.seqlens.tolist() == [4, 2]
+    for b, n in enumerate((4, 2)):
+        p = cache.block_table[b, 0].item()
+        assert bool(cache.pool[p, :n].view(torch.uint8).any(-1).all()) and not cache.pool[p, n:].any()
