@@ -72,7 +72,8 @@ __device__ __forceinline__ void pair_at(const mla_rope_table& tab, int d_r, int 
 // registers (kUnits 16-byte units per lane), the sum of squares is a warp
 // reduction, and the row goes out with 16-byte stores.  Bound by HBM (one read
 // and one write of the row), for a decode step by latency.  Measured on B200: 8740
-// bf16 tokens 6.3 us (3.2 TB/s of 20 MB; eight warps a block 6.5), 32 tokens 2.5 us.
+// bf16 tokens 5.8 us (3.5 TB/s of 20 MB; 6.4 with the table read at its use), 32
+// tokens 2.3 us (2.7).
 constexpr int kWriteWarps = 4;
 
 template <typename T, int kUnits>
@@ -101,6 +102,8 @@ cache_write_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
   if (rotate) pair_at(tab, d_r, lane, &pi, &pj);
   float pa = 0.f, pb = 0.f;
   if (lane < d_r / 2) pa = Storage<T>::to_f(row[d_c + pi]), pb = Storage<T>::to_f(row[d_c + pj]);
+  // (Lanes differ in their pair, so the table's read is serialised: while those come.)
+  const uint64_t turn = rotate && lane < d_r / 2 ? tab.turn[lane] : 0;
   if (slot < 0) return;               // padding
   if (slot >= total_rows) {
     if (lane == 0) record_status(status, MLA_ERR_BOUNDS);
@@ -136,7 +139,7 @@ cache_write_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
     }
     if (rotate) {
       float c, s;
-      rope_turn_cos_sin(tab.turn[k], pos, tab.amplitude, &c, &s);
+      rope_turn_cos_sin(k == lane ? turn : tab.turn[k], pos, tab.amplitude, &c, &s);
       const float a = pa, b = pb;
       pa = a * c - b * s;
       pb = a * s + b * c;

@@ -8,8 +8,10 @@
 // A thread moves 8 pairs with 16-byte accesses and issues its loads before the
 // cosines and sines are formed, once per (token, pair) of the block, in shared
 // memory: with 128 heads that is one sincospif per 128 rotated pairs.  Measured on
-// B200: 4096 tokens x 128 heads x 64 bf16 21.4 us (6.3 TB/s, 0.96 of a copy; 25.9
-// with one row per thread); 64 x 64 rows 2.2 us, 1023 x 16 fp32 rows 3.3 us.
+// B200: 4096 tokens x 128 heads x 64 bf16 21.3 us (6.3 TB/s, 0.96 of a copy; 25.9
+// with one row per thread); 64 x 64 rows 2.1 us, 1023 x 16 fp32 rows 3.3 us.  With one
+// head (keys) the angles bound it: 1000 rows 2.0 us, 200,000 rows 23.8 us (55 with the
+// table read for every angle, 5.4 us for 1000 rows with 64 tokens a block).
 #include "kernels.h"
 #include "rope_table.cuh"
 
@@ -19,6 +21,7 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopePairs = 8;   // pairs per thread
+constexpr int kRopeSpread = 592;   // blocks, four to an SM
 
 template <typename T> struct RopeVec;   // 8 values of T as 16-byte words
 template <> struct RopeVec<__nv_bfloat16> {
@@ -81,6 +84,10 @@ rope_vec_kernel(const __grid_constant__ mla_rope_table tab, const T* __restrict_
   const bool live = tl < toks && tok < n_tokens;
   const bool inter = tab.layout == MLA_ROPE_INTERLEAVED;
   const int o1 = inter ? 16 * g : 8 * g, o2 = inter ? 16 * g + 8 : half + 8 * g;
+  // This thread's angles: one pair, every groups-th token.  (Lanes differ in their
+  // pair, so the table's read is serialised: once, before the wait.)
+  const int groups = kRopeThreads / half, pair = threadIdx.x % half;
+  const uint64_t turn = tab.turn[pair];
   pdl_wait();
   RopeVec<T> v1[kBlocks], v2[kBlocks];
 #pragma unroll
@@ -92,13 +99,12 @@ rope_vec_kernel(const __grid_constant__ mla_rope_table tab, const T* __restrict_
       v2[k].load(p + o2);
     }
   }
-  for (int i = threadIdx.x; i < toks * half; i += kRopeThreads) {
-    const int64_t t = tok0 + i / half;
-    if (t < n_tokens) {
+  for (int t = threadIdx.x / half; t < toks; t += groups) {
+    if (tok0 + t < n_tokens && threadIdx.x < groups * half) {
       float2 cs;
-      rope_turn_cos_sin(tab.turn[i % half], pos[t], tab.amplitude, &cs.x, &cs.y);
+      rope_turn_cos_sin(turn, pos[tok0 + t], tab.amplitude, &cs.x, &cs.y);
       if (transpose) cs.y = -cs.y;
-      s_cs[i] = cs;
+      s_cs[t * half + pair] = cs;
     }
   }
   __syncthreads();
@@ -180,7 +186,11 @@ cudaError_t launch_rope(const mla_rope_table& tab, int64_t n_tokens, int H, cons
   if (tab.d_r % 16 == 0 && rows16(x, xt, xh, sizeof(T)) && rows16(y, yt, yh, sizeof(T))) {
     const int rows = kRopeThreads / (tab.d_r / 16);
     const int heads = H < rows ? H : rows;
-    const int toks = rows / heads;
+    // With few heads a block's angles take several rounds of its threads; blocks of
+    // fewer tokens, while they all run at once, share them out.
+    const int most = rows / heads, once = kRopeThreads / (tab.d_r / 2);
+    const int64_t spread = (n_tokens + kRopeSpread - 1) / kRopeSpread;
+    const int toks = int(spread >= most || once >= most ? most : spread > once ? spread : once);
     // Two rows a thread where a token has that many heads: twice the loads in
     // flight and half the angles.
     const int blocks = sizeof(T) == 2 && H >= 2 * heads ? 2 : 1;
