@@ -276,6 +276,10 @@ cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
   float g[16];
   load_gamma(gamma, lane * 8, 8, g);
   load_gamma(gamma, 256 + lane * 8, 8, g + 8);
+  // This lane's pair.  (Lanes differ, so the table's read is serialised: while x comes.)
+  int ra = lane, rc = lane + kDr / 2;
+  const uint64_t turn = kDr > 0 && rotate ? tab.turn[lane] : 0;
+  if (kDr > 0 && rotate) pair_at(tab, kDr, lane, &ra, &rc);
   if (first < 0) {
     if (tid == 0) record_status(status, MLA_ERR_BOUNDS);
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -291,10 +295,6 @@ cache_write8_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
     unpack16<__nv_bfloat16, 8>(row[lane], *reinterpret_cast<float(*)[8]>(f));
     unpack16<__nv_bfloat16, 8>(row[lane + 32], *reinterpret_cast<float(*)[8]>(f + 8));
   };
-  // This lane's pair (read once: lanes differ, so the table read is serialised).
-  int ra = lane, rc = lane + kDr / 2;
-  const uint64_t turn = kDr > 0 && rotate ? tab.turn[lane] : 0;
-  if (kDr > 0 && rotate) pair_at(tab, kDr, lane, &ra, &rc);
   // The loops over a warp's rows stay rolled: a page is written once, so what
   // its code costs is mostly the fetching of it.
   float amax = 0.f;
