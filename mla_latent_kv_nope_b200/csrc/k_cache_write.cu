@@ -157,8 +157,8 @@ cache_write_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
 // in flight at once; held in registers, a block filled an SM and 150 pages took two
 // waves), each warp norms its own, the page's largest magnitude is reduced over the
 // block and the cluster, the new exponent fixed, and the codes written.  Measured on
-// B200: 64 tokens, one a page, 4.0 us; 8740 prompt tokens 8.0 us (9.2 with one block a
-// page), 1000 tokens of one prompt 4.9 us (6.8).  If the page held rows before and its
+// B200: 64 tokens, one a page, 3.7 us; 8740 prompt tokens 8.0 us (9.2 with one block a
+// page), 1000 tokens of one prompt 4.7 us (6.8).  If the page held rows before and its
 // scale grows, those rows are rescaled first by a power of two, which is exact for the
 // rotary keys and for codes that stay normal E4M3 values and rounds the others once more.
 constexpr int k8Dc = 512;
