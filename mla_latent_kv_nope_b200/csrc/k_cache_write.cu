@@ -442,9 +442,17 @@ cudaError_t launch_cache_write_fp8(const mla_rope_table* tab, const __nv_bfloat1
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 2 : 1;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               int(S::kSmem));
-    if (e != cudaSuccess) return e;
+    if constexpr (S::kSmem > 48 * 1024) {   // more than a launch may ask for unannounced
+      static bool attr_done[64] = {false};  // of this kernel, by device
+      int dev = 0;
+      if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+      if (!attr_done[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
+        if (e != cudaSuccess) return e;
+        attr_done[dev] = true;
+      }
+    }
     return cudaLaunchKernelEx(&cfg, kernel, t, int(tab != nullptr), x, x_stride, T_rows, gamma, eps,
                               query_start, seqlens, B, cap, pm, pool, page_scales, status);
   };
