@@ -446,7 +446,7 @@ MLA_API int mla_cache_write_paged(const mla_dims* dims, int32_t T, const void* x
  * Shape of both: bf16, d_c = 512, d_r = 64 or 0.  page_scales of pages that are read must
  * be positive powers of two (as the write leaves them).  Precision: each query
  * row and the probabilities enter the 8-bit products as sums of two 8-bit terms
- * (the query as E4M3 + E4M3, exact to 2^-18 of its row's largest value; a
+ * (the query as E4M3 + E4M3, exact to 2^-18 of its row's largest value or to 2^-70; a
  * probability as E4M3 + E5M2, 2^-7 of itself at most and a few times less on
  * average), with fp32 sums; queries must be finite. */
 MLA_API int mla_cache_write_fp8_paged(const mla_dims* dims, int32_t T, const void* x,

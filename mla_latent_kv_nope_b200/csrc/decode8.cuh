@@ -188,11 +188,32 @@ __device__ __forceinline__ float split_probabilities(const uint32_t (&x)[32], fl
   return sum.x + sum.y;
 }
 
-// Exponent of a query row whose largest bf16 magnitude has the bits `top`: the
-// smallest k with top <= 448 * 2^k = 1.75 * 2^(8 + k), kept where 2^k and 2^-k
-// are normal (top = m 2^(e - 127), 7 mantissa bits, m <= 1.75 up to 96 / 128).
+// The power of two 2^k that a query row is held in units of follows its latent
+// part, but no further down than where fp32 holds everything made of it: the
+// scaled rotary part stays below 2^(kRopeLead + 9), so that its products with
+// keys in units of a page scale of 2^-40 are finite, and 2^k times such a scale
+// and the softmax scale stays a normal number.  A row whose latent part is zero, or
+// 2^kRopeLead times smaller than its rotary part, or below 2^-51, is held in
+// larger units than its latent part needs, which then loses at most 2^-10 of a
+// unit: 2^-57 of the rotary part's largest value, or 2^-70.
+constexpr int kRopeLead = 40, kMinQueryExp = -60;
+
+// What the rotary part's largest magnitude (its bf16 bits) counts for beside the
+// latent part's: 2^-kRopeLead of itself, in bits.
+__device__ __forceinline__ uint32_t rope_magnitude(uint32_t top) {
+  constexpr uint32_t lead = uint32_t(kRopeLead) << 7;
+  return top > lead ? top - lead : 0u;
+}
+// Exponent of a row whose largest bf16 magnitude has the bits `top`: the smallest k with
+// top <= 448 * 2^k = 1.75 * 2^(8 + k) (top = m 2^(e - 127), 7 mantissa bits, m <= 1.75
+// up to 96 / 128), within [kMinQueryExp, 120].
 __device__ __forceinline__ int query_exponent(uint32_t top) {
-  return min(max(int(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 96u), -120), 120);
+  return min(max(int(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 96u), kMinQueryExp), 120);
+}
+// log2 of the scores' factor: never 0, so that a masked key's -inf stays -inf (scores
+// that a smaller factor would make are 0 beside any other).
+__device__ __forceinline__ float score_factor(float row_scale, float page_scale) {
+  return fmaxf(row_scale * page_scale, 1.17549435e-38f);
 }
 __device__ __forceinline__ float exp2i(int k) { return __uint_as_float(uint32_t(127 + k) << 23); }
 

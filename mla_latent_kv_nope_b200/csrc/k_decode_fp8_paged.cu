@@ -10,10 +10,10 @@
 // 8-bit products without widening.  The codes go to the tensor cores as they
 // lie in the cache (kind::f8f6f4, twice the 16-bit rate); what is not 8 bits is
 // split into two terms, x = hi + lo:
-//   * a query row times a power of two (largest value in (224, 448]) into E4M3 +
-//     E4M3: a bf16 value has 8 significant bits and each term holds 4, so hi + lo
-//     is exact for values within 2^10 of the largest, and off by at most 2^-18 of
-//     it below;
+//   * a query row times a power of two (largest latent value in (224, 448], smaller
+//     where the rotary part is 2^40 times larger) into E4M3 + E4M3: a bf16 value
+//     has 8 significant bits and each term holds 4, so hi + lo is exact for values
+//     within 2^10 of the largest, and off by at most 2^-18 of it below;
 //   * a probability into E4M3 + E5M2: hi is off by at most 2^-4 of p, lo by 2^-3
 //     of that, 2^-7 of p together (1.4e-3 of the output in a simulation of scores
 //     with a deviation of 0.3 to 3.5, as for bf16 probabilities).
@@ -418,11 +418,18 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
           // Largest magnitude of the row: bf16 bits order like their magnitudes.
 #pragma unroll
           for (int x = 0; x < 8; ++x) top[r] = max_magnitude2(top[r], wd[r][x]);
+          top[r] = larger_half(top[r]);
+          if (kDr) {
+            uint32_t rope = 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) rope = max_magnitude2(rope, rd[r][x]);
+            top[r] = max(top[r], rope_magnitude(larger_half(rope)));
+          }
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           // (The whole warp has read both rows once it has their maxima.)
-          top[r] = __reduce_max_sync(0xffffffffu, larger_half(top[r]));
+          top[r] = __reduce_max_sync(0xffffffffu, top[r]);
           const int k = query_exponent(top[r]);
           inv[r] = __float2bfloat162_rn(exp2i(-k));
           if (lane == 0) factor[8 * warp + r0 + r] = exp2i(k);
@@ -502,7 +509,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes,
 #pragma unroll
         for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(x[j]));
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        const float f = row_scale * sc, lsc = log2f(sc);
+        const float f = score_factor(row_scale, sc), lsc = log2f(sc);
         float mt = mx * f + lsc;                        // log2 of the largest p * scale
         float* s_part = s_max + sb * 4 * 64 + row;      // [4 parts][64 rows]
         s_part[(2 * pg + part) * 64] = mt;

@@ -287,6 +287,15 @@ decode8_64_kernel(const __grid_constant__ CUtensorMap tm_codes,
         top = max_magnitude2(max_magnitude2(max_magnitude2(max_magnitude2(top, b.x), b.y), b.z), b.w);
       }
       top = larger_half(top);
+      if (kDr) {
+        uint32_t rope = 0;
+#pragma unroll
+        for (int j = 0; j < kDr / 16; ++j) {
+          const uint4 a = unit(64 + 2 * j + half);
+          rope = max_magnitude2(max_magnitude2(max_magnitude2(max_magnitude2(rope, a.x), a.y), a.z), a.w);
+        }
+        top = max(top, rope_magnitude(larger_half(rope)));
+      }
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
       const int k = query_exponent(top);
       const __nv_bfloat162 inv = __float2bfloat162_rn(exp2i(-k));
@@ -357,7 +366,7 @@ decode8_64_kernel(const __grid_constant__ CUtensorMap tm_codes,
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(x[j]));
-        const float f = row_scale * sc, lsc = log2f(sc);
+        const float f = score_factor(row_scale, sc), lsc = log2f(sc);
         // log2 of the largest p * scale of the row's 64 keys.
         float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f + lsc;
         mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));

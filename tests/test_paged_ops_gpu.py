@@ -693,6 +693,101 @@ def test_decode_fp8_paged_uneven(kind):
         assert np.linalg.norm(f64(o[b]) - ref) <= 5e-3 * np.linalg.norm(ref)
 
 
+# lse = (log2 l + r - 6.75) ln 2 with l = n 2^39 and r = -32.25: log2 l < 48 is off by an ulp
+# of 2^-18, the rest by half an ulp of numbers below 16, and the combine adds a few of 2^-21.
+ZERO_LSE = 2.0 * 2.0 ** -18
+
+
+def zero_pages(lens, H, d_r, zero_blocks):
+    """make_pages with the rows of blocks `zero_blocks` as the writer leaves zero latents: zero
+    codes and a scale of 2^-40 (rotary keys as they are)."""
+    pool, scales, table, rows = make_pages(lens, H, d_r, seed=H + d_r + 5)
+    for b, n in enumerate(lens):
+        for j in zero_blocks:
+            m = min(PAGE, n - j * PAGE)
+            if m <= 0:
+                continue
+            p = table[b, j].item()
+            pool[p, :m, :512] = 0
+            k = pool[p, :m, 512:].contiguous().view(torch.bfloat16)
+            pool[p, :m, 512:] = (k.float() * (scales[p] * 2.0 ** 40)).to(torch.bfloat16).view(torch.uint8)
+            scales[p] = 2.0 ** -40
+            rows[b][j * PAGE:j * PAGE + m, :512] = 0
+    return pool, scales, table, rows
+
+
+@pytest.mark.parametrize("H", [16, 64, 128])
+@pytest.mark.parametrize("q_pe", [1.0, 300.0, 2.0 ** 100])
+def test_decode_fp8_paged_zero_latent_query(H, q_pe):
+    """Heads whose latent query is zero (all of them in the first sequence, some among
+    others in the second), with rotary parts of any size: their scores are the rotary
+    products alone."""
+    lens = [65, 200, 1, 63]
+    pool, scales, table, rows = make_pages(lens, H, 64, seed=H)
+    dims = mla.Dims(4, H, 512, 64, 128, 128, table.shape[1] * PAGE, "bf16")
+    q = randn(H + 1, 4, H, 576, dtype=torch.bfloat16)
+    q[0, :, :512] = 0
+    q[1, 3::5, :512] = 0
+    q[3, ::2, :512] = 1e-30                 # next to nothing, but not zero
+    zero = ~(q[:, :, :512].abs() > 1e-20).any(-1)
+    q[..., 512:] *= torch.where(zero, q_pe, 1.0)[..., None].to(torch.bfloat16)
+    scale = 1 / math.sqrt(192) / max(q_pe / 300, 1.0)
+    o, lse = run_decode8(dims, q, pool, scales, table, i32(lens), scale)
+    assert mla.get_device_status() == 0
+    check_attend(o, lse, q, rows, lens, scale)
+    # Where the latent part is zero the two terms leave nothing out: fp32 sums alone.
+    for b, n in enumerate(lens):
+        h = zero[b].cpu().numpy()
+        qb = f64(q[b])[h]
+        if not len(qb):
+            continue
+        ref, ref_lse, z = attend64(qb, rows[b], scale)
+        dz = scale * F32 * (np.abs(qb) @ np.abs(rows[b]).T).max(-1)
+        p = np.exp(z - ref_lse[:, None])
+        lim = (p * (2.0 ** -7 + 2.0 ** -11 + 2 * dz[:, None])) @ np.abs(rows[b][:, :512])
+        lim += 2.0 ** -15 * n * p.max(-1, keepdims=True) * np.abs(rows[b][:, :512]).max()
+        assert np.all(np.abs(f64(o[b])[h] - ref) <= lim + 1e-6)
+        assert np.all(np.abs(f64(lse[b])[h] - ref_lse) <= 2 * dz + 1e-5)
+
+
+@pytest.mark.parametrize("H,d_r", [(16, 64), (64, 64), (128, 64), (64, 0), (128, 0)])
+@pytest.mark.parametrize("scale", [0.07, 1e-44])
+def test_decode_fp8_paged_zero_query_and_zero_pages(H, d_r, scale):
+    """Zero queries over pages of zero latents with a partly filled last page (a request of
+    zeros): every key weighs the same, lse = log n.  Scores of next to nothing the same."""
+    lens = [1, 63, 65, 300, 64]
+    pool, scales, table, rows = zero_pages(lens, H, d_r, (0, 1, 4))
+    dims = mla.Dims(5, H, 512, d_r, 128, 128, table.shape[1] * PAGE, "bf16")
+    q = randn(3, 5, H, 512 + d_r, dtype=torch.bfloat16)
+    q[:3] = 0
+    q[3, 1::3] = 0
+    o, lse = run_decode8(dims, q, pool, scales, table, i32(lens), scale)
+    assert mla.get_device_status() == 0
+    check_attend(o, lse, q, rows, lens, scale)
+    for b in range(3):
+        assert bool((lse[b] - math.log(lens[b])).abs().max() <= ZERO_LSE)
+        assert not o[b].any()
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_paged_cache_step_of_zeros(H):
+    """A request of zero rows and zero queries through PagedCache and DecodeStep (a dummy
+    step before serving): zeros, and lse = log n."""
+    dims = mla.Dims(2, H, 512, 64, 128, 128, 128, "bf16")
+    tab = mla.rope_table(64)
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    cache = mla.PagedCache(dims, num_pages=4, max_tokens=128, fp8=True, table=tab)
+    step = mla.DecodeStep(dims, (0.05 * randn(1, H, 128, 512)).to(torch.bfloat16),
+                          (0.05 * randn(2, H, 128, 512)).to(torch.bfloat16), rope_table=tab)
+    cache.plan(i32([70, 5]), tokens=75)
+    cache.write(z(75, 576))
+    out = step(z(2, H, 128), z(2, H, 64), cache.last_positions(), cache.pool, cache.seqlens,
+               block_table=cache.block_table, page_scales=cache.page_scales)
+    assert mla.get_device_status() == 0 and not out.any()
+    want = torch.tensor([math.log(70), math.log(5)], device="cuda")[:, None]
+    assert bool((step.lse - want).abs().max() <= ZERO_LSE)
+
+
 def test_decode_fp8_paged_bad_page_and_long_length():
     """A page id outside the pool reads as zeros and is reported; a length past the
     capacity is cut to it."""
