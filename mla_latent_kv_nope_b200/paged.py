@@ -47,7 +47,8 @@ class PagedCache:
         self.positions = torch.full((max_tokens,), -1, **i32)
         self.slots = torch.full((max_tokens,), -1, dtype=torch.int64, device=device)
         self.token_request = torch.full((max_tokens,), -1, **i32)
-        self._planned = None     # rows that the next write must have
+        self._open = False       # a step is planned
+        self._planned = None     # rows that its write must have, if they were stated
         self._last = torch.zeros(B, **i32)
         self._ws = torch.zeros(b.plan_pages_workspace_bytes(), dtype=torch.uint8, device=device)
 
@@ -55,18 +56,21 @@ class PagedCache:
         """plan_pages in place: request r gets new_lens[r] more tokens (int32 [B]), at most
         ``tokens`` in all (max_tokens if None): the rows that write() will be given.  A
         step of more is not begun and records MLA_ERR_BOUNDS."""
-        self._planned = tokens
+        self._open = False       # until the plan is made
         T = self.positions.shape[0] if tokens is None else tokens
         if not 0 <= T <= self.positions.shape[0]:
             raise ValueError(f"tokens must be in [0, {self.positions.shape[0]}], got {T}")
         b.plan_pages(self.seqlens, new_lens, self.block_table, self.free_pages, self.free_count,
                      self.num_pages, self.query_start, self.positions[:T], self.slots[:T],
                      self.seqlens, self.free_count, self._ws, token_request=self.token_request[:T])
+        self._open, self._planned = True, tokens
 
     def write(self, x) -> None:
         """The planned tokens' rows: x [T, d_c + d_r], requests in order; T = plan's
         ``tokens`` (without it, T must not be less than the step's tokens).  Rows
         behind the last token are not stored."""
+        if not self._open:
+            raise ValueError("no step is planned")
         if self._planned is not None and x.shape[0] != self._planned:
             raise ValueError(f"x has {x.shape[0]} rows, the step was planned for {self._planned}")
         if self.page_scales is not None:

@@ -236,3 +236,35 @@ def test_paged_cache_counts_rows(monkeypatch):
     for n in (-1, 17):
         with pytest.raises(ValueError, match="tokens"):
             cache.plan(new, tokens=n)
+
+
+def test_paged_cache_write_after_a_failed_plan(monkeypatch):
+    """A step that was refused is not written, whatever its size: the last step's places and
+    lengths are still there."""
+    calls = []
+
+    def plan_pages(*a, **kw):
+        if a[7].shape[0] == 5:
+            raise mla.MLAError("mla_plan_pages", 1, "invalid argument")
+    monkeypatch.setattr(bd, "plan_pages", plan_pages)
+    for name in ("cache_write_paged", "cache_write_fp8_paged"):
+        monkeypatch.setattr(bd, name, lambda d, x, *a: calls.append(x.shape[0]))
+    new = torch.ones(2, dtype=torch.int32)
+    for fp8 in (False, True):
+        cache = mla.PagedCache(mla.Dims(2, 16, 512, 64, 128, 128, 128, "bf16"), 4, 16, fp8=fp8,
+                               device="cpu")
+        with pytest.raises(ValueError, match="no step"):
+            cache.write(torch.zeros(2, 576))
+        cache.plan(new, tokens=2)
+        with pytest.raises(ValueError, match="tokens"):
+            cache.plan(new, tokens=17)
+        for n in (2, 17):
+            with pytest.raises(ValueError, match="no step"):
+                cache.write(torch.zeros(n, 576))
+        with pytest.raises(mla.MLAError):
+            cache.plan(new, tokens=5)
+        with pytest.raises(ValueError, match="no step"):
+            cache.write(torch.zeros(5, 576))
+        cache.plan(new, tokens=2)
+        cache.write(torch.zeros(2, 576))
+    assert calls == [2, 2]
