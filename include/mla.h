@@ -414,12 +414,21 @@ MLA_API int mla_release_pages(int32_t B, int32_t* seqlens, const int32_t* releas
  * table NULL).  slots[t] < 0 skips the token; a slot past the pool is skipped
  * and records MLA_ERR_BOUNDS.  Rows without a slot stay as they are.  Each slot
  * at most once per call (of two, either row or a mix of both is stored).
- * MLA_F32 needs d_r % 4 == 0. */
+ * MLA_F32 needs d_r % 4 == 0.
+ * mla_cache_write_paged_step is the same for a step whose size only the device
+ * knows: planned [1] int32 (the last entry of mla_plan_pages' query_start, or NULL) is
+ * the number of its tokens, and if T (at least 1) is less MLA_ERR_BOUNDS is recorded; the
+ * T rows are stored. */
 MLA_API int mla_cache_write_paged(const mla_dims* dims, int32_t T, const void* x,
                                   int64_t x_stride, const float* gamma, float eps,
                                   const mla_rope_table* table, const int32_t* positions,
                                   const int64_t* slots, void* cache_pool, int64_t num_pages,
                                   void* stream);
+MLA_API int mla_cache_write_paged_step(const mla_dims* dims, int32_t T, const void* x,
+                                       int64_t x_stride, const float* gamma, float eps,
+                                       const mla_rope_table* table, const int32_t* positions,
+                                       const int64_t* slots, const int32_t* planned,
+                                       void* cache_pool, int64_t num_pages, void* stream);
 
 /* --- paged 8-bit latent cache --------------------------------------------------------
  * The 8-bit cache in pages, with one fp32 scale for each page (block of 64

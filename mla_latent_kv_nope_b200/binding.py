@@ -34,8 +34,8 @@ EXPORTED = (
     "mla_cache_append_fp8", "mla_decode_fp8", "mla_fold_output_weights",
     "mla_out_proj_folded_workspace_bytes", "mla_out_proj_folded", "mla_prefill_workspace_bytes",
     "mla_prefill", "mla_rope_init", "mla_rope", "mla_plan_pages_workspace_bytes",
-    "mla_plan_pages", "mla_release_pages", "mla_cache_write_paged", "mla_cache_write_fp8_paged",
-    "mla_decode_fp8_paged",
+    "mla_plan_pages", "mla_release_pages", "mla_cache_write_paged", "mla_cache_write_paged_step",
+    "mla_cache_write_fp8_paged", "mla_decode_fp8_paged",
 )
 
 PAGE_ROWS = 64   # rows per page of a paged latent cache (one decode work tile)
@@ -166,6 +166,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                           P, P, SZ, P]),
         "mla_release_pages": (ctypes.c_int, [I32, P, P, P, I32, P, I32, P, I64, P]),
         "mla_cache_write_paged": (ctypes.c_int, [D, I32, P, I64, P, F, P, P, P, P, I64, P]),
+        "mla_cache_write_paged_step": (ctypes.c_int, [D, I32, P, I64, P, F, P, P, P, P, P, I64, P]),
         "mla_cache_write_fp8_paged": (ctypes.c_int, [D, I32, P, I64, P, F, P, P, P, P, I32, P, P,
                                                      I64, P]),
         "mla_decode_fp8_paged": (ctypes.c_int, [D, P, P, P, I64, P, I32, P, F, ctypes.c_int, P,
@@ -189,7 +190,7 @@ def _load_calls(lib) -> None:
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
     mod.init(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
-        "mla_rope", "mla_plan_pages", "mla_cache_write_paged", "mla_cache_write_fp8_paged",
+        "mla_rope", "mla_plan_pages", "mla_cache_write_paged_step", "mla_cache_write_fp8_paged",
         "mla_decode_fp8_paged")))
     _calls = mod
 
@@ -679,24 +680,27 @@ def release_pages(seqlens, release, block_table, free_pages, free_count, num_pag
 
 
 def cache_write_paged(dims: Dims, x, gamma, positions, slots, cache_pool, table=None, eps=1e-6,
-                      stream=None):
+                      stream=None, planned=None):
     """mla_cache_write_paged: the rows [RMSNorm(x_c) * gamma || RoPE(x_r, position)] of
     projected tokens x [T, d_c + d_r] to rows ``slots`` (int64, -1: none) of
-    cache_pool [num_pages, 64, d_c + d_r].  Without a table x_r is stored as it is."""
+    cache_pool [num_pages, 64, d_c + d_r].  Without a table x_r is stored as it is.
+    ``planned`` (int32 [1], query_start's last entry) is the number of the step's tokens: a
+    T of less is recorded as MLA_ERR_BOUNDS."""
     if (_calls is not None and stream is None
             and (table is None or isinstance(table, RopeTable))):
         st = _calls.cache_write_paged(dims.address, x, gamma, positions, slots, cache_pool, table,
-                                      eps)
+                                      eps, planned)
         if st is not None:
             return _check("mla_cache_write_paged", st) if st else None
     dev = _device(x, "x")
     dt, R, n = dims.torch_dtype, dims.R, cache_pool.shape[0]
     px, T, sx = _rows(x, dt, R, dev)
-    _launch("mla_cache_write_paged", dev, stream, dims.ref, T, px, sx,
+    _launch("mla_cache_write_paged_step", dev, stream, dims.ref, T, px, sx,
             None if gamma is None else _arg(gamma, _F32, (dims.d_c,), "gamma", dev), eps,
             _table_ptr(table),
             None if positions is None else _arg(positions, _I32, (T,), "positions", dev),
             _arg(slots, _I64, (T,), "slots", dev),
+            None if planned is None else _arg(planned, _I32, (1,), "planned", dev),
             _arg(cache_pool, dt, (n, PAGE_ROWS, R), "cache_pool", dev), n)
 
 

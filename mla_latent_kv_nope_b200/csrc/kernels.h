@@ -140,12 +140,14 @@ cudaError_t launch_page_release(int32_t* seqlens, const int32_t* release, int B,
                                 int* status, cudaStream_t stream);
 
 // Latent rows of T projected tokens into pages (see mla_cache_write_paged and
-// mla_cache_write_fp8_paged); `tab` is null for rows that are rotated already.
+// mla_cache_write_fp8_paged); `tab` is null for rows that are rotated already, `planned`
+// where the step's size is not checked.
 template <typename T>
 cudaError_t launch_cache_write(const mla_rope_table* tab, const T* x, int64_t x_stride,
                                const float* gamma, float eps, const int32_t* positions,
-                               const int64_t* slots, int T_rows, int d_c, int d_r,
-                               int64_t total_rows, T* pool, int* status, cudaStream_t stream);
+                               const int64_t* slots, const int32_t* planned, int T_rows, int d_c,
+                               int d_r, int64_t total_rows, T* pool, int* status,
+                               cudaStream_t stream);
 cudaError_t launch_cache_write_fp8(const mla_rope_table* tab, const __nv_bfloat16* x,
                                    int64_t x_stride, int T_rows, const float* gamma, float eps,
                                    const int32_t* query_start, const int32_t* seqlens, int B,

@@ -583,20 +583,30 @@ int mla_cache_write_paged(const mla_dims* d, int32_t T, const void* x, int64_t x
                           const float* gamma, float eps, const mla_rope_table* table,
                           const int32_t* positions, const int64_t* slots, void* cache_pool,
                           int64_t num_pages, void* stream) {
+  return mla_cache_write_paged_step(d, T, x, x_stride, gamma, eps, table, positions, slots, nullptr,
+                                    cache_pool, num_pages, stream);
+}
+
+int mla_cache_write_paged_step(const mla_dims* d, int32_t T, const void* x, int64_t x_stride,
+                               const float* gamma, float eps, const mla_rope_table* table,
+                               const int32_t* positions, const int64_t* slots,
+                               const int32_t* planned, void* cache_pool, int64_t num_pages,
+                               void* stream) {
   int st = check_write(d, T, x, x_stride, gamma, eps, table, cache_pool, num_pages);
   if (st) return st;
-  if (T == 0) return MLA_OK;
+  if (T == 0) return planned ? MLA_ERR_INVALID_ARG : MLA_OK;
   if (!slots || (table && !positions)) return MLA_ERR_INVALID_ARG;
-  if (!aligned_to(slots, 8) || !aligned_to(positions, 4)) return MLA_ERR_ALIGNMENT;
+  if (!aligned_to(slots, 8) || !aligned_to(positions, 4) || !aligned_to(planned, 4))
+    return MLA_ERR_ALIGNMENT;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t rows = num_pages * kTileKeys;
   if (d->dtype == MLA_BF16)
     return cuda_status(launch_cache_write<__nv_bfloat16>(
-        table, static_cast<const __nv_bfloat16*>(x), x_stride, gamma, eps, positions, slots, T,
-        d->d_c, d->d_r, rows, static_cast<__nv_bfloat16*>(cache_pool), status_ptr(), s));
+        table, static_cast<const __nv_bfloat16*>(x), x_stride, gamma, eps, positions, slots,
+        planned, T, d->d_c, d->d_r, rows, static_cast<__nv_bfloat16*>(cache_pool), status_ptr(), s));
   return cuda_status(launch_cache_write<float>(
-      table, static_cast<const float*>(x), x_stride, gamma, eps, positions, slots, T, d->d_c,
-      d->d_r, rows, static_cast<float*>(cache_pool), status_ptr(), s));
+      table, static_cast<const float*>(x), x_stride, gamma, eps, positions, slots, planned, T,
+      d->d_c, d->d_r, rows, static_cast<float*>(cache_pool), status_ptr(), s));
 }
 
 int mla_cache_write_fp8_paged(const mla_dims* d, int32_t T, const void* x, int64_t x_stride,

@@ -22,7 +22,7 @@ using at::ScalarType;
 
 decltype(&mla_rope) f_rope;
 decltype(&mla_plan_pages) f_plan_pages;
-decltype(&mla_cache_write_paged) f_write;
+decltype(&mla_cache_write_paged_step) f_write;
 decltype(&mla_cache_write_fp8_paged) f_write8;
 decltype(&mla_decode_fp8_paged) f_decode8;
 
@@ -186,10 +186,10 @@ PyObject* plan_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
       static_cast<int32_t*>(count_out), ws->data_ptr(), ws->nbytes(), c.stream()));
 }
 
-// cache_write_paged(dims, x, gamma, positions, slots, cache_pool, table, eps)
+// cache_write_paged(dims, x, gamma, positions, slots, cache_pool, table, eps, planned)
 PyObject* cache_write_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Call c;
-  MLA_SLOW_UNLESS(n == 8);
+  MLA_SLOW_UNLESS(n == 9);
   const mla_dims* d = c.dims(a[0]);
   MLA_SLOW_UNLESS(c.ok);
   const int64_t R = int64_t(d->d_c) + d->d_r;
@@ -203,10 +203,11 @@ PyObject* cache_write_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void* pool = c.arg(a[5], scalar(d), {pages, kPageRows, R});
   const mla_rope_table* tab = a[6] == Py_None ? nullptr : c.table(a[6]);
   const float eps = c.real(a[7]);
+  const void* planned = c.ok ? c.optional(a[8], ScalarType::Int, {1}) : nullptr;
   MLA_SLOW_UNLESS(c.ok);
   return status(f_write(d, int32_t(T), x, stride, static_cast<const float*>(gamma), eps, tab,
-                        static_cast<const int32_t*>(pos), static_cast<const int64_t*>(slots), pool,
-                        pages, c.stream()));
+                        static_cast<const int32_t*>(pos), static_cast<const int64_t*>(slots),
+                        static_cast<const int32_t*>(planned), pool, pages, c.stream()));
 }
 
 // cache_write_fp8_paged(dims, x, gamma, query_start, seqlens, block_table, cache_pool,

@@ -67,12 +67,15 @@ class PagedCache:
 
     def write(self, x) -> None:
         """The planned tokens' rows: x [T, d_c + d_r], requests in order; T = plan's
-        ``tokens`` (without it, T must not be less than the step's tokens).  Rows
-        behind the last token are not stored."""
+        ``tokens``.  Without it T is at least 1 and not less than the step's tokens, which
+        only the device knows: fewer rows record MLA_ERR_BOUNDS.  Rows behind the last
+        token are not stored."""
         if not self._open:
             raise ValueError("no step is planned")
         if self._planned is not None and x.shape[0] != self._planned:
             raise ValueError(f"x has {x.shape[0]} rows, the step was planned for {self._planned}")
+        if self._planned is None and x.shape[0] == 0:
+            raise ValueError("no rows: plan an empty step with tokens=0")
         if self.page_scales is not None:
             b.cache_write_fp8_paged(self.dims, x, self.gamma, self.query_start, self.seqlens,
                                     self.block_table, self.pool, self.page_scales, self.table,
@@ -80,7 +83,8 @@ class PagedCache:
         else:
             T = x.shape[0]
             b.cache_write_paged(self.dims, x, self.gamma, self.positions[:T], self.slots[:T],
-                                self.pool, self.table, self.eps)
+                                self.pool, self.table, self.eps, None,
+                                self.query_start[-1:] if self._planned is None else None)
 
     def last_positions(self):
         """Position of each request's last token (-1 without one): the query's in a decode step."""

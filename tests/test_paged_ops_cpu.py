@@ -268,3 +268,34 @@ def test_paged_cache_write_after_a_failed_plan(monkeypatch):
         cache.plan(new, tokens=2)
         cache.write(torch.zeros(2, 576))
     assert calls == [2, 2]
+
+
+def test_write_step_refusals(lib):
+    """mla_cache_write_paged_step: mla_cache_write_paged's checks, and those of `planned`."""
+    def write(T=3, slots=GOOD, planned=GOOD, x=GOOD, eps=1e-6):
+        return lib.mla_cache_write_paged_step(dims(), T, x, 576, None, eps, None, None, slots, planned,
+                                              GOOD, 4, None)
+    assert write(T=0, planned=None) == OK
+    for kw in (dict(T=0), dict(T=-1), dict(slots=None), dict(x=None), dict(eps=-1.0)):
+        assert write(**kw) == INVALID, kw
+    for kw in (dict(planned=ODD), dict(x=P(0x10008)), dict(slots=P(0x10004))):
+        assert write(**kw) == ALIGN, kw
+
+
+def test_paged_cache_states_the_step_to_the_device(monkeypatch):
+    """Without a stated size the write of 16-bit pages gets the step's tokens from the plan."""
+    calls = []
+    monkeypatch.setattr(bd, "plan_pages", lambda *a, **kw: None)
+    monkeypatch.setattr(bd, "cache_write_paged",
+                        lambda d, x, g, pos, slots, pool, tab, eps, stream=None, planned=None:
+                        calls.append(planned))
+    cache = mla.PagedCache(mla.Dims(2, 16, 512, 64, 128, 128, 128, "bf16"), 4, 16, device="cpu")
+    new = torch.ones(2, dtype=torch.int32)
+    cache.plan(new)
+    with pytest.raises(ValueError, match="tokens=0"):
+        cache.write(torch.zeros(0, 576))
+    cache.write(torch.zeros(3, 576))
+    cache.plan(new, tokens=2)
+    cache.write(torch.zeros(2, 576))
+    assert calls[0].shape == (1,) and calls[0].data_ptr() == cache.query_start[2:].data_ptr()
+    assert calls[1:] == [None]

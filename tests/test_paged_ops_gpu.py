@@ -1109,3 +1109,34 @@ def test_paged_cache_step_of_a_stated_size(fp8):
     for b, n in enumerate((4, 2)):
         p = cache.block_table[b, 0].item()
         assert bool(cache.pool[p, :n].view(torch.uint8).any(-1).all()) and not cache.pool[p, n:].any()
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_paged_cache_reports_missing_rows(fp8):
+    """A step planned without its size and written with fewer rows than its tokens is
+    reported; as many or more rows are not, nor is a captured step's replay."""
+    dims = mla.Dims(2, 16, 512, 64, 128, 128, 128, "bf16")
+    cache = mla.PagedCache(dims, num_pages=4, max_tokens=16, fp8=fp8, table=mla.rope_table(64))
+    x, new = randn(1, 16, 576, dtype=torch.bfloat16), i32([3, 2])
+    for rows, want in ((4, 7), (5, 0), (1, 7), (16, 0)):
+        cache.plan(new)
+        cache.write(x[:rows])
+        assert mla.get_device_status() == want, rows
+        cache.release(i32([1, 1]))
+    cache.plan(new)
+    with pytest.raises(ValueError, match="tokens=0"):
+        cache.write(x[:0])
+    cache.release(i32([1, 1]))
+    cache.plan(i32([0, 0]), tokens=0)
+    cache.write(x[:0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.plan(new)
+        cache.write(x[:6])
+    for n, want in (([3, 3], 0), ([3, 4], 7), ([0, 0], 0), ([6, 0], 0)):
+        new.copy_(i32(n))
+        g.replay()
+        assert mla.get_device_status() == want, n
+        assert cache.seqlens.tolist() == n
+        cache.release(i32([1, 1]))
+    assert mla.get_device_status() == 0
