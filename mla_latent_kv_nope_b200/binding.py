@@ -176,8 +176,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    _lib = lib
     _load_calls(lib)
+    _lib = lib           # once both are there
     return lib
 
 

@@ -299,3 +299,15 @@ def test_paged_cache_states_the_step_to_the_device(monkeypatch):
     cache.write(torch.zeros(2, 576))
     assert calls[0].shape == (1,) and calls[0].data_ptr() == cache.query_start[2:].data_ptr()
     assert calls[1:] == [None]
+
+
+def test_missing_calls_module_fails_every_time(tmp_path, monkeypatch):
+    """The library is not loaded without the module of the short operators' calls, at the
+    second attempt as little as at the first."""
+    monkeypatch.setattr(bd, "_lib", None)
+    monkeypatch.setattr(bd, "_calls", None)
+    monkeypatch.setattr(bd, "_HERE", str(tmp_path))
+    for _ in range(2):
+        with pytest.raises(RuntimeError, match="missing"):
+            bd.load_library(bld.LIB_PATH)
+        assert bd._lib is None and bd._calls is None
