@@ -16,6 +16,8 @@ from dataclasses import dataclass
 
 import torch
 
+from .build import calls_name
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmla_b200.so")
 
@@ -183,7 +185,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 
 def _load_calls(lib) -> None:
     global _calls
-    at = os.path.join(_HERE, "_calls.so")
+    at = os.path.join(_HERE, calls_name())
     if not os.path.exists(at):
         raise RuntimeError(f"{at} is missing: build it with mla_latent_kv_nope_b200.build.build()")
     spec = importlib.util.spec_from_file_location("_calls", at)

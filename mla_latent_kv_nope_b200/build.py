@@ -1,7 +1,7 @@
 """Build the in-tree shared library ``libmla_b200.so`` for sm_100a.
 
-``_calls.so`` beside it is a small CPython module over torch's headers: the checks
-and calls of the short operators (csrc/py_calls.cpp), compiled with g++.
+A small CPython module beside it (``calls_name()``), over torch's headers, holds the
+checks and calls of the short operators (csrc/py_calls.cpp), compiled with g++.
 
 Each ``csrc/*.cu`` file is compiled to an object in parallel with
 ``nvcc -gencode arch=compute_100a,code=sm_100a -lineinfo -O3`` and linked into
@@ -23,7 +23,6 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libmla_b200.so")
 CALLS_SRC = os.path.join(CSRC, "py_calls.cpp")
-CALLS_PATH = os.path.join(HERE, "_calls.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -55,12 +54,20 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps() + [__file__])
 
 
+def calls_name() -> str:
+    """File name of the calls module: it reads torch's and Python's structures, so it is
+    built and loaded for one version of each only."""
+    import torch
+    return f"_calls.torch-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}"
+
+
 def build_calls(force: bool = False) -> str:
     """Compile the CPython module of the short operators' calls.  Raises on failure."""
     deps = [CALLS_SRC, os.path.join(INCLUDE, "mla.h"), __file__]
-    if (not force and os.path.exists(CALLS_PATH)
-            and all(os.path.getmtime(p) <= os.path.getmtime(CALLS_PATH) for p in deps)):
-        return CALLS_PATH
+    path = os.path.join(HERE, calls_name())
+    if (not force and os.path.exists(path)
+            and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps)):
+        return path
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
@@ -68,7 +75,7 @@ def build_calls(force: bool = False) -> str:
     dirs = [os.path.join(root, "include"),
             os.path.join(root, "include", "torch", "csrc", "api", "include"),
             os.path.join(cuda, "include"), sysconfig.get_path("include")]
-    tmp = CALLS_PATH + ".tmp"
+    tmp = path + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(f"-isystem{d}" for d in dirs), CALLS_SRC, "-o", tmp, f"-L{libs}", "-lc10", "-lc10_cuda",
@@ -76,8 +83,8 @@ def build_calls(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS_PATH)
-    return CALLS_PATH
+    os.replace(tmp, path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:

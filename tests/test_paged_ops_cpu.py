@@ -3,6 +3,7 @@ fake (never dereferenced) pointers through the C ABI, host tensors through the
 binding, and the rope table's angles against their formulas in 64 bits."""
 import ctypes
 import math
+import sysconfig
 
 import numpy as np
 import pytest
@@ -311,3 +312,19 @@ def test_missing_calls_module_fails_every_time(tmp_path, monkeypatch):
         with pytest.raises(RuntimeError, match="missing"):
             bd.load_library(bld.LIB_PATH)
         assert bd._lib is None and bd._calls is None
+
+
+def test_calls_module_of_another_torch_is_not_loaded(monkeypatch):
+    """The module reads torch's structures: one that was built against another torch (or
+    Python) is as good as missing."""
+    monkeypatch.setattr(bd, "_lib", None)
+    monkeypatch.setattr(bd, "_calls", None)
+    assert bd.load_library() is not None
+    for where, name, value in ((torch, "__version__", "0.0.0"),
+                               (sysconfig, "get_config_var", lambda k: ".cpython-20.so")):
+        with monkeypatch.context() as m:
+            m.setattr(where, name, value)
+            m.setattr(bd, "_lib", None)
+            m.setattr(bd, "_calls", None)
+            with pytest.raises(RuntimeError, match="missing"):
+                bd.load_library()
