@@ -1,7 +1,8 @@
 """Build the in-tree shared library ``libmla_b200.so`` for sm_100a.
 
 A small CPython module beside it (``calls_name()``), over torch's headers, holds the
-checks and calls of the short operators (csrc/py_calls.cpp), compiled with g++.
+checks and calls of the short operators for Python (csrc/py_calls.cpp), compiled with
+g++.  The library itself needs neither: without torch only it is built.
 
 Each ``csrc/*.cu`` file is compiled to an object in parallel with
 ``nvcc -gencode arch=compute_100a,code=sm_100a -lineinfo -O3`` and linked into
@@ -12,6 +13,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -88,9 +90,16 @@ def build_calls(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
-    """Compile and link the library (and the calls module); returns the library's
-    path.  Raises on failure."""
-    build_calls(force)
+    """Compile and link the library, then the calls module where there is torch;
+    returns the library's path.  Raises on failure."""
+    build_library(force, verbose, extra_flags)
+    if importlib.util.find_spec("torch") is not None:
+        build_calls(force)
+    return LIB_PATH
+
+
+def build_library(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
+    """Compile and link the library alone.  Raises on failure."""
     if not force and up_to_date():
         return LIB_PATH
     nvcc = _nvcc()

@@ -3,6 +3,8 @@ fake (never dereferenced) pointers through the C ABI, host tensors through the
 binding, and the rope table's angles against their formulas in 64 bits."""
 import ctypes
 import math
+import subprocess
+import sys
 import sysconfig
 
 import numpy as np
@@ -328,3 +330,20 @@ def test_calls_module_of_another_torch_is_not_loaded(monkeypatch):
             m.setattr(bd, "_calls", None)
             with pytest.raises(RuntimeError, match="missing"):
                 bd.load_library()
+
+
+def test_library_builds_without_torch(tmp_path):
+    """The C ABI's library needs no torch; the calls module is for Python and is left out."""
+    code = f"""
+import importlib.util, sys
+sys.modules["torch"] = None
+spec = importlib.util.spec_from_file_location("build_alone", {bld.__file__!r})
+b = importlib.util.module_from_spec(spec)
+spec.loader.exec_module(b)
+b.HERE = {str(tmp_path)!r}
+b.up_to_date = lambda: True
+print(b.build() == b.LIB_PATH)
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert r.stdout.strip() == "True", r.stderr
+    assert not list(tmp_path.iterdir())
