@@ -133,13 +133,15 @@ __device__ __forceinline__ bool find_segments(int32_t len0, const int32_t* seqle
       scratch[kWarps] = b, scratch[kWarps + 1] = e - n, scratch[kWarps + 2] = len;
     __syncthreads();
     base += chunk;
-    if (u0 < base) break;      // u0 < total, so some chunk holds it
+    // Some chunk holds u0 < total, unless a length has changed since it was counted (by a
+    // call on another stream that should have been ordered): then the walk ends here.
+    if (u0 < base || b0 + kThreads >= B) break;
   }
   *out = Segments{seqlens, B,  int(scratch[kWarps]),         cap, scratch[kWarps + 1],
                   u0,      u1, int32_t(scratch[kWarps + 2]), 0,   0,
                   0,       0};
   __syncthreads();             // before the scratch is used for anything else
-  return true;
+  return u0 < base;
 }
 
 // Two fp32 operations in one instruction.
