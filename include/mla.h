@@ -375,7 +375,8 @@ MLA_API int mla_rope(int32_t dtype, const mla_rope_table* table, int64_t n_token
  * step, as in a captured graph); other outputs must not overlap inputs.
  * free_pages has free_capacity entries and is not changed.  If the step cannot
  * be served as a whole (more pages needed than are free, more than T tokens, a
- * sequence past 64 * max_blocks, a negative length or count) nothing is taken:
+ * sequence past 64 * max_blocks, a negative length or count) nothing is taken (the
+ * attention stops at its dims' cache_capacity, so that should be 64 * max_blocks):
  * MLA_ERR_BOUNDS is recorded in the device status word, every place gets -1,
  * query_start is 0, and lengths, count and block_table stay.  A page id outside
  * [0, num_pages) gives its tokens slot -1 and records MLA_ERR_BOUNDS.
@@ -446,7 +447,7 @@ MLA_API int mla_cache_write_paged_step(const mla_dims* dims, int32_t T, const vo
  * for k^R and for codes that stay normal E4M3 numbers, the others are rounded to
  * nearest even once more).  Rows behind a sequence's last and pages without new
  * tokens stay as they are.  No page may be written for two requests in one
- * call.  query_start ascends.  A request whose lengths do not fit (negative counts, more than T rows,
+ * call.  query_start ascends.  T = 0 does nothing.  A request whose lengths do not fit (negative counts, more than T rows,
  * seqlens[b] below its count or above cache_capacity) is skipped, a page id
  * outside the pool skips that page; both record MLA_ERR_BOUNDS.
  * mla_decode_fp8_paged is mla_decode_paged over the dequantised rows [c~ || k^R]:
@@ -456,8 +457,11 @@ MLA_API int mla_cache_write_paged_step(const mla_dims* dims, int32_t T, const vo
  * be positive powers of two (as the write leaves them).  Precision: each query
  * row and the probabilities enter the 8-bit products as sums of two 8-bit terms
  * (the query as E4M3 + E4M3, exact to 2^-18 of its row's largest value or to 2^-70; a
- * probability as E4M3 + E5M2, 2^-7 of itself at most and a few times less on
- * average), with fp32 sums; queries must be finite. */
+ * probability times its page's scale as E4M3 + E5M2), with fp32 sums.  Such a weight
+ * is off by at most 2^-7 of itself (a few times less on average) plus 2^-10.7 of the
+ * largest one of its tile of 64 keys (128 above 64 heads), so that far below that a
+ * key adds nothing to o; lse and the sum that o is divided by are fp32.  Queries must
+ * be finite. */
 MLA_API int mla_cache_write_fp8_paged(const mla_dims* dims, int32_t T, const void* x,
                                       int64_t x_stride, const float* gamma, float eps,
                                       const mla_rope_table* table, const int32_t* query_start,

@@ -104,7 +104,8 @@ cache_write_kernel(const __grid_constant__ mla_rope_table tab, int rotate,
     const int c = (lane + 32 * u) * kVec;
     v[u] = c < d_c ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
   }
-  // Everything else that is read is asked for before the first use of x.
+  // Slot, position and rotary pair are asked for before the first use of x (gamma, the
+  // same for every token, where the row is stored).
   const int64_t slot = slots[t];
   const int64_t pos = rotate ? positions[t] : 0;
   int pi = lane, pj = lane + d_r / 2;

@@ -15,8 +15,9 @@
 //     has 8 significant bits and each term holds 4, so hi + lo is exact for values
 //     within 2^10 of the largest, and off by at most 2^-18 of it below;
 //   * a probability into E4M3 + E5M2: hi is off by at most 2^-4 of p, lo by 2^-3
-//     of that, 2^-7 of p together (1.4e-3 of the output in a simulation of scores
-//     with a deviation of 0.3 to 3.5, as for bf16 probabilities).
+//     of that, 2^-7 of p together, or 2^-17 where lo is below E5M2's normal numbers
+//     (1.4e-3 of the output in a simulation of scores with a deviation of 0.3 to
+//     3.5, as for bf16 probabilities).
 // So both products cost as many tensor cycles as 16-bit ones, but the cache
 // is read, staged and fed at one byte per value and no thread touches it.  The
 // RoPE part is a bf16 product into the same accumulator.
@@ -32,8 +33,9 @@
 // largest so far, below which nothing is left to add.  A move costs a wait for
 // the last product, so the window is as wide as the two formats allow: E5M2 lo
 // holds what E4M3 hi loses down to 2^-16, so a tile whose maximum lies 2^13
-// below the reference still keeps three bits of keys 2^7 below that.  With E4M3
-// for lo the window was 2^7 wide and two tiles in three moved some row of 128
+// below the reference still keeps three bits of keys 2^7 below that; 2^-17 is
+// then 2^-10.7 of its largest, and keys 2^11 below that are lost from O (the sum l,
+// in fp32, counts them).  With E4M3 for lo the window was 2^7 wide and two tiles in three moved some row of 128
 // (scores with a deviation of 1.7); now one in forty does.
 //
 // Structure: a cluster of two CTAs (128 heads, 64 each) shares every product

@@ -788,6 +788,40 @@ def test_paged_cache_step_of_zeros(H):
     assert bool((step.lse - want).abs().max() <= ZERO_LSE)
 
 
+@pytest.mark.parametrize("H,d", [(H, d) for H in (64, 128) for d in (7.0, 9.5, 10.5, 12.0)])
+def test_decode_fp8_paged_weights_far_below_their_tile(H, d):
+    """The stated bound of a weight, where it is worst: tiles whose one large key lies at the
+    lower edge of the reference's window (5.2 binades below the first tile's keys, which put
+    the reference 7.75 above them, with a window of 13), the others d binades below that."""
+    lens, per = [20 * PAGE], 2 if H > 64 else 1
+    pool, scales, table, rows = make_pages(lens, H, 64, seed=H, spread=0)
+    dims = mla.Dims(1, H, 512, 64, 128, 128, table.shape[1] * PAGE, "bf16")
+    scale = 1 / math.sqrt(192)
+    q = torch.zeros(1, H, 576, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 512] = 16
+    j = np.arange(lens[0])
+    tile = j // (per * PAGE)
+    bits = np.where(tile == 0, 0.0, np.where(j % (per * PAGE) == 5, -5.2, -5.2 - d))
+    want = bits * math.log(2) / scale / 16
+    rows[0][:, 512:] = 0
+    for t in range(20):
+        pg, s = table[0, t].item(), scales[table[0, t]].item()
+        k = torch.zeros(PAGE, 64, dtype=torch.bfloat16)
+        k[:, 0] = torch.from_numpy(want[t * PAGE:(t + 1) * PAGE] / s).to(torch.bfloat16)
+        pool[pg, :, 512:] = k.view(torch.uint8).cuda()
+        rows[0][t * PAGE:(t + 1) * PAGE, 512] = k[:, 0].double().numpy() * s
+    o, lse = run_decode8(dims, q, pool, scales, table, i32(lens), scale, 1)
+    assert mla.get_device_status() == 0
+    ref, ref_lse, z = attend64(f64(q[0]), rows[0], scale)
+    p = np.exp(z - ref_lse[:, None])
+    top = np.stack([p[:, tile == t].max(-1) for t in range(tile.max() + 1)], -1)[:, tile]
+    # (fp16 before the two terms 2^-11, the score 2^-20 of itself.)
+    c = np.abs(rows[0][:, :512])
+    lim = (p * (2.0 ** -7 + 2.0 ** -11 + F32 * np.abs(z)) + 2.0 ** -10.7 * top) @ c
+    assert np.all(np.abs(f64(o[0]) - ref) <= lim)
+    assert np.all(np.abs(f64(lse[0]) - ref_lse) <= F32 * np.abs(z).max() + 1e-5)
+
+
 def test_decode_fp8_paged_bad_page_and_long_length():
     """A page id outside the pool reads as zeros and is reported; a length past the
     capacity is cut to it."""
