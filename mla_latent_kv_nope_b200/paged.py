@@ -48,6 +48,7 @@ class PagedCache:
         self.free_pages = torch.arange(num_pages - 1, -1, -1, **i32)   # page 0 is taken first
         self.free_count = torch.full((1,), num_pages, **i32)
         self.query_start = torch.zeros(B + 1, **i32)
+        self._step_tokens = self.query_start[B:]     # [1]: the planned step's tokens
         self.positions = torch.full((max_tokens,), -1, **i32)
         self.slots = torch.full((max_tokens,), -1, dtype=torch.int64, device=device)
         self.token_request = torch.full((max_tokens,), -1, **i32)
@@ -88,7 +89,7 @@ class PagedCache:
             T = x.shape[0]
             b.cache_write_paged(self.dims, x, self.gamma, self.positions[:T], self.slots[:T],
                                 self.pool, self.table, self.eps, None,
-                                self.query_start[-1:] if self._planned is None else None)
+                                self._step_tokens if self._planned is None else None)
 
     def last_positions(self):
         """Position of each request's last token (-1 without one): the query's in a decode step."""
