@@ -10,7 +10,7 @@
 // SMs, but half the loads and less power, so a higher clock.
 // Measured on B200 (decode alone, graphs of ten): 64 sequences of 512 to 32768
 // tokens with 64 heads 176-181 us, against 222 with pairs; 4 x 4096 tokens with 16
-// heads 11.7 us, against 14.4.  A tile takes 2490 cycles at 1.8 GHz (memory would
+// heads 11.9 us, against 14.4.  A tile takes 2490 cycles at 1.8 GHz (memory would
 // allow 1750), so the tensor pipe bounds long sequences; a short one is bound by
 // its start, about 9 us from the lengths to the first partial.  Tried and not
 // faster: a fourth stage in the memory of the staged query (182 us), four more warps
