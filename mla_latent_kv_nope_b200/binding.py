@@ -800,10 +800,13 @@ class DecodeStep:
                       if rope_table is not None else None)
         self._side = torch.cuda.Stream(device=device) if overlap else None
 
-    def append(self, h, cache, seqlens, block_table=None, scales=None, page_scales=None):
+    def _no_append(self, page_scales):
         if page_scales is not None or self.rope_table is not None:
             raise ValueError("8-bit pages and rope tables take their rows from "
                              "cache_write_fp8_paged / cache_write_paged, before the step (h=None)")
+
+    def append(self, h, cache, seqlens, block_table=None, scales=None, page_scales=None):
+        self._no_append(page_scales)
         if scales is not None:
             cache_append_fp8(self.dims, h, self.W_DKV, self.gamma, cache, scales, seqlens,
                              self.ws_append, self.eps, self.rope_base)
@@ -853,6 +856,8 @@ class DecodeStep:
         whose rows are written before the step."""
         if page_scales is not None and block_table is None:
             raise ValueError("page_scales needs a block_table")
+        if h is not None:
+            self._no_append(page_scales)     # before the fork: a capture must be joined
         if self._side is None:
             if h is not None:
                 self.append(h, cache, seqlens, block_table, scales, page_scales)

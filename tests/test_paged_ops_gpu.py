@@ -1174,3 +1174,23 @@ def test_paged_cache_reports_missing_rows(fp8):
         assert cache.seqlens.tolist() == n
         cache.release(i32([1, 1]))
     assert mla.get_device_status() == 0
+
+
+def test_decode_step_refuses_an_append_before_it_forks():
+    """The refusal of h is what a capture reports, and the step is usable after it."""
+    dims, tab = mla.Dims(2, 16, 512, 64, 128, 128, 128, "bf16"), mla.rope_table(64)
+    bf = lambda i, *s: randn(i, *s, dtype=torch.bfloat16)  # noqa: E731
+    cache = mla.PagedCache(dims, num_pages=4, max_tokens=64, fp8=True, table=tab)
+    step = mla.DecodeStep(dims, bf(1, 16, 128, 512), bf(2, 16, 128, 512), bf(3, 576, 256),
+                          rope_table=tab)
+    cache.plan(i32([3, 2]), tokens=5)
+    cache.write(bf(4, 5, 576))
+    args = (bf(5, 2, 16, 128), bf(6, 2, 16, 64), cache.last_positions(), cache.pool, cache.seqlens)
+    kw = dict(block_table=cache.block_table, page_scales=cache.page_scales)
+    want = step(*args, **kw).clone()
+    for call in (step, step.capture):
+        with pytest.raises(ValueError, match="before the step"):
+            call(*args, h=bf(7, 2, 256), **kw)
+    step.out.zero_()
+    step.capture(*args, **kw).replay()
+    assert torch.equal(step.out, want) and mla.get_device_status() == 0
