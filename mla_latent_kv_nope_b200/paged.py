@@ -22,18 +22,14 @@ from . import binding as b
 
 
 class PagedCache:
-    """dims: B requests at most, cache_capacity tokens of each (whole pages); num_pages
-    pages of 64 rows; max_tokens new tokens in one step.  ``fp8`` holds 8-bit rows.  ``table`` (see
+    """dims: B requests at most, cache_capacity tokens of each; num_pages pages of 64
+    rows; max_tokens new tokens in one step.  ``fp8`` holds 8-bit rows.  ``table`` (see
     rope_table) rotates the rotary keys; None stores them as they come."""
 
     def __init__(self, dims: b.Dims, num_pages: int, max_tokens: int, fp8=False, gamma=None,
                  table=None, eps=1e-6, device="cuda"):
         self.dims, self.num_pages, self.gamma, self.table, self.eps = dims, num_pages, gamma, table, eps
-        # A plan fills whole pages; rows of a last one past the capacity would not be attended.
-        if dims.cache_capacity % b.PAGE_ROWS:
-            raise ValueError(f"cache_capacity must be a multiple of {b.PAGE_ROWS}, "
-                             f"got {dims.cache_capacity}")
-        B, blocks = dims.B, dims.cache_capacity // b.PAGE_ROWS
+        B, blocks = dims.B, (dims.cache_capacity + b.PAGE_ROWS - 1) // b.PAGE_ROWS
         i32 = dict(dtype=torch.int32, device=device)
         if fp8:
             self.pool = torch.zeros(num_pages, b.PAGE_ROWS, dims.d_c + 2 * dims.d_r,

@@ -347,11 +347,3 @@ print(b.build() == b.LIB_PATH)
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
     assert r.stdout.strip() == "True", r.stderr
     assert not list(tmp_path.iterdir())
-
-
-@pytest.mark.parametrize("capacity", [1, 100, 129])
-def test_paged_cache_capacity_is_whole_pages(capacity):
-    """The plan knows whole pages, the attention the capacity: between the two a sequence
-    would keep tokens that are never attended."""
-    with pytest.raises(ValueError, match="multiple of 64"):
-        mla.PagedCache(mla.Dims(2, 16, 512, 64, 128, 128, capacity, "bf16"), 4, 16, device="cpu")
