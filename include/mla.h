@@ -375,14 +375,16 @@ MLA_API int mla_rope(int32_t dtype, const mla_rope_table* table, int64_t n_token
  * step, as in a captured graph); other outputs must not overlap inputs.
  * free_pages has free_capacity entries and is not changed.  If the step cannot
  * be served as a whole (more pages needed than are free, more than T tokens, a
- * sequence past 64 * max_blocks, a negative length or count) nothing is taken (the
- * attention stops at its dims' cache_capacity, so that should be 64 * max_blocks):
+ * sequence past 64 * max_blocks, a negative length or count) nothing is taken:
  * MLA_ERR_BOUNDS is recorded in the device status word, every place gets -1,
  * query_start is 0, and lengths, count and block_table stay.  A page id outside
  * [0, num_pages) gives its tokens slot -1 and records MLA_ERR_BOUNDS.
  * workspace: mla_plan_pages_workspace_bytes() bytes, zeroed by the caller before
  * its first use; every call leaves it zero, and calls that may run at the same
  * time need one each.
+ * mla_plan_pages_capped is mla_plan_pages with the longest sequence allowed stated, 0 <
+ * capacity <= 64 * max_blocks: the attention stops at its dims' cache_capacity, so
+ * where that ends inside a page a plan should too.
  * mla_release_pages returns the pages of every request with release[b] != 0 to
  * the end of free_pages (ascending requests and blocks), sets those block_table
  * entries to -1 and seqlens[b] to 0, and updates free_count in place; if a page
@@ -396,6 +398,14 @@ MLA_API int mla_plan_pages(int32_t B, const int32_t* seqlens, const int32_t* new
                            int32_t T, int32_t* query_start, int32_t* positions, int64_t* slots,
                            int32_t* token_request, int32_t* seqlens_out, int32_t* free_count_out,
                            void* workspace, size_t workspace_bytes, void* stream);
+MLA_API int mla_plan_pages_capped(int32_t B, const int32_t* seqlens, const int32_t* new_lens,
+                                  int32_t* block_table, int32_t max_blocks, int64_t capacity,
+                                  const int32_t* free_pages, int32_t free_capacity,
+                                  const int32_t* free_count, int64_t num_pages, int32_t T,
+                                  int32_t* query_start, int32_t* positions, int64_t* slots,
+                                  int32_t* token_request, int32_t* seqlens_out,
+                                  int32_t* free_count_out, void* workspace,
+                                  size_t workspace_bytes, void* stream);
 MLA_API int mla_release_pages(int32_t B, int32_t* seqlens, const int32_t* release,
                               int32_t* block_table, int32_t max_blocks, int32_t* free_pages,
                               int32_t free_capacity, int32_t* free_count, int64_t num_pages,

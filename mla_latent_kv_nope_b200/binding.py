@@ -36,7 +36,7 @@ EXPORTED = (
     "mla_cache_append_fp8", "mla_decode_fp8", "mla_fold_output_weights",
     "mla_out_proj_folded_workspace_bytes", "mla_out_proj_folded", "mla_prefill_workspace_bytes",
     "mla_prefill", "mla_rope_init", "mla_rope", "mla_plan_pages_workspace_bytes",
-    "mla_plan_pages", "mla_release_pages", "mla_cache_write_paged", "mla_cache_write_paged_step",
+    "mla_plan_pages", "mla_plan_pages_capped", "mla_release_pages", "mla_cache_write_paged", "mla_cache_write_paged_step",
     "mla_cache_write_fp8_paged", "mla_decode_fp8_paged",
 )
 
@@ -166,6 +166,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "mla_plan_pages_workspace_bytes": (SZ, []),
         "mla_plan_pages": (ctypes.c_int, [I32, P, P, P, I32, P, I32, P, I64, I32, P, P, P, P, P,
                                           P, P, SZ, P]),
+        "mla_plan_pages_capped": (ctypes.c_int, [I32, P, P, P, I32, I64, P, I32, P, I64, I32, P, P,
+                                                 P, P, P, P, P, SZ, P]),
         "mla_release_pages": (ctypes.c_int, [I32, P, P, P, I32, P, I32, P, I64, P]),
         "mla_cache_write_paged": (ctypes.c_int, [D, I32, P, I64, P, F, P, P, P, P, I64, P]),
         "mla_cache_write_paged_step": (ctypes.c_int, [D, I32, P, I64, P, F, P, P, P, P, P, I64, P]),
@@ -192,7 +194,7 @@ def _load_calls(lib) -> None:
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
     mod.init(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
-        "mla_rope", "mla_plan_pages", "mla_cache_write_paged_step", "mla_cache_write_fp8_paged",
+        "mla_rope", "mla_plan_pages_capped", "mla_cache_write_paged_step", "mla_cache_write_fp8_paged",
         "mla_decode_fp8_paged")))
     _calls = mod
 
@@ -641,15 +643,16 @@ def plan_pages_workspace_bytes() -> int:
 
 def plan_pages(seqlens, new_lens, block_table, free_pages, free_count, num_pages, query_start,
                positions, slots, seqlens_out, free_count_out, workspace, token_request=None,
-               stream=None):
+               stream=None, capacity=None):
     """mla_plan_pages: take the pages this step's new tokens need off the free
     list into block_table [B, max_blocks], and fill query_start [B+1],
     positions [T] (int32) and slots [T] (int64); seqlens_out and
-    free_count_out may be seqlens and free_count."""
+    free_count_out may be seqlens and free_count.  ``capacity`` is the longest sequence
+    (None: 64 * max_blocks)."""
     if _calls is not None and stream is None:
         st = _calls.plan_pages(seqlens, new_lens, block_table, free_pages, free_count, num_pages,
                                query_start, positions, slots, seqlens_out, free_count_out,
-                               workspace, token_request)
+                               workspace, token_request, capacity)
         if st is not None:
             return _check("mla_plan_pages", st) if st else None
     dev = _device(seqlens, "seqlens")
@@ -657,9 +660,10 @@ def plan_pages(seqlens, new_lens, block_table, free_pages, free_count, num_pages
     mb = block_table.shape[-1]
     b, one, t = (B,), (1,), (T,)
     ws, nws = _ws_arg(workspace, dev)
-    _launch("mla_plan_pages", dev, stream, B, _arg(seqlens, _I32, b, "seqlens", dev),
+    _launch("mla_plan_pages_capped", dev, stream, B, _arg(seqlens, _I32, b, "seqlens", dev),
             _arg(new_lens, _I32, b, "new_lens", dev),
             _arg(block_table, _I32, (B, mb), "block_table", dev), mb,
+            mb * PAGE_ROWS if capacity is None else capacity,
             _arg(free_pages, _I32, (F,), "free_pages", dev), F,
             _arg(free_count, _I32, one, "free_count", dev), num_pages, T,
             _arg(query_start, _I32, (B + 1,), "query_start", dev),

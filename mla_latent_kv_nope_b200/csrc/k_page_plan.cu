@@ -72,6 +72,7 @@ struct PlanArgs {
   int B;
   int32_t* block_table;
   int max_blocks;
+  int64_t capacity;         // the longest sequence, at most 64 * max_blocks < 2^31
   const int32_t* free_pages;
   int free_capacity;
   const int32_t* free_count;
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     const int32_t Lb = a.seqlens[b], nb = a.new_lens[b];
     if (b == tid) L0 = Lb, n0 = nb;
     const int64_t L = Lb, n = nb;
-    if (L < 0 || n < 0 || L + n > int64_t(a.max_blocks) * kTileKeys || L + n > INT32_MAX) bad = 1;
+    if (L < 0 || n < 0 || L + n > a.capacity) bad = 1;
     else tok += n, need += pages_of(L + n) - pages_of(L);
   }
   block_sum2(tok, need, bad, s_red);
@@ -265,17 +266,18 @@ page_release_kernel(int32_t* seqlens, const int32_t* __restrict__ release, int B
 }  // namespace
 
 cudaError_t launch_page_plan(const int32_t* seqlens, const int32_t* new_lens, int B,
-                             int32_t* block_table, int max_blocks, const int32_t* free_pages,
-                             int free_capacity, const int32_t* free_count, int64_t num_pages,
-                             int T, int32_t* query_start, int32_t* positions, int64_t* slots,
+                             int32_t* block_table, int max_blocks, int64_t capacity,
+                             const int32_t* free_pages, int free_capacity,
+                             const int32_t* free_count, int64_t num_pages, int T,
+                             int32_t* query_start, int32_t* positions, int64_t* slots,
                              int32_t* token_request, int32_t* seqlens_out,
                              int32_t* free_count_out, void* workspace, int* status,
                              cudaStream_t stream) {
   const int grid = T > 0 ? (T + kPlanTokens - 1) / kPlanTokens : 1;
   // A request with n new tokens takes at most n / 64 + 1 new pages.
   const int64_t most = int64_t(T) / kTileKeys + B;
-  const PlanArgs a{seqlens, new_lens, B, block_table, max_blocks, free_pages, free_capacity,
-                   free_count, num_pages, T, query_start, positions, slots, token_request,
+  const PlanArgs a{seqlens, new_lens, B, block_table, max_blocks, capacity, free_pages,
+                   free_capacity, free_count, num_pages, T, query_start, positions, slots, token_request,
                    seqlens_out, free_count_out, static_cast<uint32_t*>(workspace),
                    seqlens_out == seqlens || free_count_out == free_count,
                    int((most + grid - 1) / grid), status};

@@ -128,9 +128,10 @@ cudaError_t launch_rope(const mla_rope_table& tab, int64_t n_tokens, int H, cons
 // Page plans (see mla_plan_pages, mla_release_pages).  The workspace is one
 // zeroed 32-bit ticket.
 cudaError_t launch_page_plan(const int32_t* seqlens, const int32_t* new_lens, int B,
-                             int32_t* block_table, int max_blocks, const int32_t* free_pages,
-                             int free_capacity, const int32_t* free_count, int64_t num_pages,
-                             int T, int32_t* query_start, int32_t* positions, int64_t* slots,
+                             int32_t* block_table, int max_blocks, int64_t capacity,
+                             const int32_t* free_pages, int free_capacity,
+                             const int32_t* free_count, int64_t num_pages, int T,
+                             int32_t* query_start, int32_t* positions, int64_t* slots,
                              int32_t* token_request, int32_t* seqlens_out,
                              int32_t* free_count_out, void* workspace, int* status,
                              cudaStream_t stream);

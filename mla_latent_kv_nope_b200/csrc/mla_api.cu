@@ -519,8 +519,23 @@ int mla_plan_pages(int32_t B, const int32_t* seqlens, const int32_t* new_lens,
                    int32_t* query_start, int32_t* positions, int64_t* slots,
                    int32_t* token_request, int32_t* seqlens_out, int32_t* free_count_out,
                    void* workspace, size_t workspace_bytes, void* stream) {
+  return mla_plan_pages_capped(B, seqlens, new_lens, block_table, max_blocks,
+                               int64_t(max_blocks) * kTileKeys, free_pages, free_capacity,
+                               free_count, num_pages, T, query_start, positions, slots,
+                               token_request, seqlens_out, free_count_out, workspace,
+                               workspace_bytes, stream);
+}
+
+int mla_plan_pages_capped(int32_t B, const int32_t* seqlens, const int32_t* new_lens,
+                          int32_t* block_table, int32_t max_blocks, int64_t capacity,
+                          const int32_t* free_pages, int32_t free_capacity,
+                          const int32_t* free_count, int64_t num_pages, int32_t T,
+                          int32_t* query_start, int32_t* positions, int64_t* slots,
+                          int32_t* token_request, int32_t* seqlens_out, int32_t* free_count_out,
+                          void* workspace, size_t workspace_bytes, void* stream) {
   int st = check_page_list(B, max_blocks, free_capacity, num_pages);
   if (st) return st;
+  if (capacity <= 0 || capacity > int64_t(max_blocks) * kTileKeys) return MLA_ERR_INVALID_ARG;
   if (T < 0 || !seqlens || !new_lens || !block_table || (free_capacity && !free_pages) ||
       !free_count || !query_start || (T && (!positions || !slots)) || !seqlens_out ||
       !free_count_out)
@@ -532,8 +547,8 @@ int mla_plan_pages(int32_t B, const int32_t* seqlens, const int32_t* new_lens,
     if (!aligned_to(p, 4)) return MLA_ERR_ALIGNMENT;
   if (!aligned_to(slots, 8)) return MLA_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < mla_plan_pages_workspace_bytes()) return MLA_ERR_WORKSPACE;
-  return cuda_status(launch_page_plan(seqlens, new_lens, B, block_table, max_blocks, free_pages,
-                                      free_capacity, free_count, num_pages, T, query_start,
+  return cuda_status(launch_page_plan(seqlens, new_lens, B, block_table, max_blocks, capacity,
+                                      free_pages, free_capacity, free_count, num_pages, T, query_start,
                                       positions, slots, token_request, seqlens_out,
                                       free_count_out, workspace, status_ptr(),
                                       static_cast<cudaStream_t>(stream)));

@@ -21,7 +21,7 @@ namespace {
 using at::ScalarType;
 
 decltype(&mla_rope) f_rope;
-decltype(&mla_plan_pages) f_plan_pages;
+decltype(&mla_plan_pages_capped) f_plan_pages;
 decltype(&mla_cache_write_paged_step) f_write;
 decltype(&mla_cache_write_fp8_paged) f_write8;
 decltype(&mla_decode_fp8_paged) f_decode8;
@@ -155,10 +155,10 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // plan_pages(seqlens, new_lens, block_table, free_pages, free_count, num_pages, query_start,
-//            positions, slots, seqlens_out, free_count_out, workspace, token_request)
+//            positions, slots, seqlens_out, free_count_out, workspace, token_request, capacity)
 PyObject* plan_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Call c;
-  MLA_SLOW_UNLESS(n == 13);
+  MLA_SLOW_UNLESS(n == 14);
   const ScalarType i32 = ScalarType::Int;
   const int64_t B = c.size(a[0], 0), blocks = c.size(a[2], 1), F = c.size(a[3], 0),
                 T = c.size(a[7], 0);
@@ -176,11 +176,12 @@ PyObject* plan_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void* count_out = c.arg(a[10], i32, {1});
   const at::Tensor* ws = c.ok ? c.tensor(a[11]) : nullptr;
   void* request = c.ok ? c.optional(a[12], i32, {T}) : nullptr;
+  const int64_t capacity = a[13] == Py_None ? blocks * kPageRows : c.integer(a[13]);
   MLA_SLOW_UNLESS(c.ok && ws->is_contiguous());
   return status(f_plan_pages(
       int32_t(B), static_cast<const int32_t*>(seq), static_cast<const int32_t*>(add),
-      static_cast<int32_t*>(table), int32_t(blocks), static_cast<const int32_t*>(free_pages),
-      int32_t(F), static_cast<const int32_t*>(count), pages, int32_t(T),
+      static_cast<int32_t*>(table), int32_t(blocks), capacity,
+      static_cast<const int32_t*>(free_pages), int32_t(F), static_cast<const int32_t*>(count), pages, int32_t(T),
       static_cast<int32_t*>(qs), static_cast<int32_t*>(pos), static_cast<int64_t*>(slots),
       static_cast<int32_t*>(request), static_cast<int32_t*>(seq_out),
       static_cast<int32_t*>(count_out), ws->data_ptr(), ws->nbytes(), c.stream()));

@@ -63,7 +63,8 @@ class PagedCache:
             raise ValueError(f"tokens must be in [0, {self.positions.shape[0]}], got {T}")
         b.plan_pages(self.seqlens, new_lens, self.block_table, self.free_pages, self.free_count,
                      self.num_pages, self.query_start, self.positions[:T], self.slots[:T],
-                     self.seqlens, self.free_count, self._ws, token_request=self.token_request[:T])
+                     self.seqlens, self.free_count, self._ws, token_request=self.token_request[:T],
+                     capacity=self.dims.cache_capacity)
         self._open, self._planned = True, tokens
 
     def write(self, x) -> None:

@@ -347,3 +347,14 @@ print(b.build() == b.LIB_PATH)
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
     assert r.stdout.strip() == "True", r.stderr
     assert not list(tmp_path.iterdir())
+
+
+def test_plan_capped_refusals(lib):
+    """mla_plan_pages_capped: mla_plan_pages' checks, and a capacity within its blocks."""
+    def plan(capacity=200, blocks=4, B=2, slots=GOOD, ws=GOOD):
+        return lib.mla_plan_pages_capped(B, GOOD, GOOD, GOOD, blocks, capacity, GOOD, 9, GOOD, 9, 8,
+                                         GOOD, GOOD, slots, None, GOOD, GOOD, ws, 256, None)
+    for kw in (dict(capacity=0), dict(capacity=-1), dict(capacity=257), dict(capacity=1 << 40),
+               dict(B=0), dict(blocks=0)):
+        assert plan(**kw) == INVALID, kw
+    assert plan(slots=P(0x10004)) == ALIGN and plan(ws=None) == WS and plan(B=65536) == UNSUP

@@ -1194,3 +1194,49 @@ def test_decode_step_refuses_an_append_before_it_forks():
     step.out.zero_()
     step.capture(*args, **kw).replay()
     assert torch.equal(step.out, want) and mla.get_device_status() == 0
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("capacity,H", [(100, 16), (1, 64), (1000, 128)])
+def test_paged_cache_stops_at_a_capacity_inside_a_page(capacity, H, fp8):
+    """A capacity that ends inside a page holds: the attention stops there, so the plan does
+    too, and a step past it takes nothing."""
+    dims = mla.Dims(2, H, 512, 64, 128, 128, capacity, "bf16")
+    tab = mla.rope_table(64)
+    cache = mla.PagedCache(dims, num_pages=40, max_tokens=2100, fp8=fp8, table=tab)
+    x = randn(1, 2100, 576, dtype=torch.bfloat16)
+    cache.plan(i32([capacity, capacity - 1]))
+    cache.write(x)
+    assert mla.get_device_status() == 0 and cache.seqlens.tolist() == [capacity, capacity - 1]
+    held = [t.clone() for t in (cache.pool, cache.block_table, cache.free_count)]
+    for new in ([1, 0], [0, 2], [1, 1]):
+        cache.plan(i32(new), tokens=2)
+        cache.write(x[:2])
+        assert mla.get_device_status() == 7, new
+        assert cache.seqlens.tolist() == [capacity, capacity - 1]
+        assert bool((cache.slots[:2] == -1).all()) and not cache.query_start.any()
+        for t, k in zip((cache.pool, cache.block_table, cache.free_count), held):
+            assert torch.equal(t, k)
+    cache.plan(i32([0, 1]), tokens=1)
+    cache.write(x[:1])
+    assert mla.get_device_status() == 0 and cache.seqlens.tolist() == [capacity, capacity]
+
+
+def test_plan_pages_capacity_argument():
+    pool = Pool([130, 5], 12, 4)
+    args = (pool.d_len, i32([1, 60]), pool.d_table, pool.d_free, pool.d_count, pool.num_pages,
+            i32([0] * 3), i32([0] * 64), torch.zeros(64, dtype=torch.int64, device="cuda"),
+            i32([0] * 2), i32([0]),
+            torch.zeros(mla.plan_pages_workspace_bytes(), dtype=torch.uint8, device="cuda"))
+    for capacity, want in ((130, 7), (131, 0), (256, 0), (None, 0)):
+        mla.plan_pages(*args, capacity=capacity)
+        assert mla.get_device_status() == want, capacity
+        assert args[9].tolist() == ([130, 5] if want else [131, 65])
+    for capacity in (0, -1, 257):
+        with pytest.raises(mla.MLAError, match="INVALID"):
+            mla.plan_pages(*args, capacity=capacity)
+    # The same with a stream of its own: the checks of the wrapper.
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    mla.plan_pages(*args, capacity=130, stream=s)
+    assert mla.get_device_status(s) == 7 and args[9].tolist() == [130, 5]
