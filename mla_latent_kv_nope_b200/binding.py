@@ -551,9 +551,9 @@ def _ws_arg(t, dev):
     return t.data_ptr(), t.nbytes
 
 
-def _launch(fn, dev, stream, *args):
+def _launch(fn, dev, stream, *args, name=None):
     """Call the library's `fn`(*args, stream) with `dev` current, on its current
-    stream unless one is given, and raise on a bad status."""
+    stream unless one is given, and raise on a bad status (as `name`, if given)."""
     f = getattr(_lib or load_library(), fn)
     if torch._C._cuda_getDevice() == dev:
         st = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
@@ -563,7 +563,7 @@ def _launch(fn, dev, stream, *args):
             st = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
                    else stream.cuda_stream)
     if st:
-        _check(fn, st)
+        _check(name or fn, st)
 
 
 def _table_ptr(table):
@@ -670,7 +670,7 @@ def plan_pages(seqlens, new_lens, block_table, free_pages, free_count, num_pages
             _arg(positions, _I32, t, "positions", dev), _arg(slots, _I64, t, "slots", dev),
             None if token_request is None else _arg(token_request, _I32, t, "token_request", dev),
             _arg(seqlens_out, _I32, b, "seqlens_out", dev),
-            _arg(free_count_out, _I32, one, "free_count_out", dev), ws, nws)
+            _arg(free_count_out, _I32, one, "free_count_out", dev), ws, nws, name="mla_plan_pages")
 
 
 def release_pages(seqlens, release, block_table, free_pages, free_count, num_pages, stream=None):
@@ -707,7 +707,8 @@ def cache_write_paged(dims: Dims, x, gamma, positions, slots, cache_pool, table=
             None if positions is None else _arg(positions, _I32, (T,), "positions", dev),
             _arg(slots, _I64, (T,), "slots", dev),
             None if planned is None else _arg(planned, _I32, (1,), "planned", dev),
-            _arg(cache_pool, dt, (n, PAGE_ROWS, R), "cache_pool", dev), n)
+            _arg(cache_pool, dt, (n, PAGE_ROWS, R), "cache_pool", dev), n,
+            name="mla_cache_write_paged")
 
 
 def cache_write_fp8_paged(dims: Dims, x, gamma, query_start, seqlens, block_table, cache_pool,

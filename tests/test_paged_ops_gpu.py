@@ -1240,3 +1240,17 @@ def test_plan_pages_capacity_argument():
     s.wait_stream(torch.cuda.current_stream())
     mla.plan_pages(*args, capacity=130, stream=s)
     assert mla.get_device_status(s) == 7 and args[9].tolist() == [130, 5]
+
+
+def test_errors_name_the_operator():
+    """A refusal names the operator, whichever way the call took."""
+    pool, dims = Pool([1], 2, 1), mla.Dims(1, 16, 512, 64, 128, 128, PAGE, "bf16")
+    n, x = i32([1]), randn(1, 1, 576, dtype=torch.bfloat16)
+    slots, mem = torch.zeros(1, dtype=torch.int64, device="cuda"), randn(2, 1, PAGE, 576, dtype=torch.bfloat16)
+    for stream in (None, torch.cuda.current_stream()):
+        with pytest.raises(mla.MLAError, match="^mla_plan_pages failed"):
+            mla.plan_pages(pool.d_len, n, pool.d_table, pool.d_free, pool.d_count, 0, i32([0, 0]), n,
+                           slots, pool.d_len, pool.d_count, i32([0] * 64), stream=stream)
+        with pytest.raises(mla.MLAError, match="^mla_cache_write_paged failed"):
+            mla.cache_write_paged(dims, x, None, n, slots, mem, eps=-1.0, stream=stream)
+    assert mla.get_device_status() == 0
