@@ -427,7 +427,8 @@ MLA_API int mla_release_pages(int32_t B, int32_t* seqlens, const int32_t* releas
  * at most once per call (of two, either row or a mix of both is stored).
  * MLA_F32 needs d_r % 4 == 0.
  * mla_cache_write_paged_step is the same for a step whose size only the device
- * knows: planned [1] int32 (the last entry of mla_plan_pages' query_start, or NULL) is
+ * knows: planned [1] int32 (the last entry of mla_plan_pages' query_start, so 4-byte
+ * aligned is enough, or NULL) is
  * the number of its tokens, and if T (at least 1) is less MLA_ERR_BOUNDS is recorded; the
  * T rows are stored. */
 MLA_API int mla_cache_write_paged(const mla_dims* dims, int32_t T, const void* x,
